@@ -6,6 +6,8 @@ The functions ``fa_fwd``, ``fa_varlen_fwd``, ``fa_fwd_strided``, ``fa_varlen_fwd
 ``fa_varlen_bwd_strided``,
 ``fa_pack_key_mask``,
 ``fa_fwd_keymask``, ``fa_bwd_keymask``, ``fa_fwd_fp8``, ``fa_decode``, ``fa_decode_paged``, ``fa_decode_workspace_size``,
+``fa_decode_fp8``, ``fa_decode_paged_fp8``, ``fa_decode_fp8_workspace_size``, ``fa_build_block_tables``,
+``fa_cache_append_paged``, ``fa_cache_append_fp8``, ``fa_cache_append_paged_fp8``,
 ``fa_bwd_workspace_size``, ``fa_varlen_bwd``,
 ``fa_bwd``, ``fa_status_string`` and ``fa_get_last_device_error`` have the
 names, argument order and meaning of the C ABI in ``include/fa.h``: pointers
@@ -70,6 +72,13 @@ _SIGS = {
     "fa_varlen_bwd_window_anchor": ([_P] * 12 + [_I] * 8 + [_F, _I, _I, _I, _I, _P], _I),
     "fa_decode": ([_P] * 7 + [_I] * 6 + [_F, _I, _I, _P], _I),
     "fa_decode_paged": ([_P] * 8 + [_I] * 8 + [_F, _I, _I, _P], _I),
+    "fa_decode_fp8_workspace_size": ([_I] * 5, ctypes.c_size_t),
+    "fa_decode_fp8": ([_P] * 9 + [_I] * 6 + [_F, _I, _I, _P], _I),
+    "fa_decode_paged_fp8": ([_P] * 10 + [_I] * 8 + [_F, _I, _I, _P], _I),
+    "fa_build_block_tables": ([_P] * 8 + [_I] * 6 + [_P], _I),
+    "fa_cache_append_paged": ([_P] * 7 + [_I] * 6 + [_P], _I),
+    "fa_cache_append_fp8": ([_P] * 11 + [_I] * 7 + [_P], _I),
+    "fa_cache_append_paged_fp8": ([_P] * 12 + [_I] * 9 + [_P], _I),
 }
 
 
@@ -273,6 +282,54 @@ def fa_decode_paged(q, k_pages, v_pages, o, lse, cache_seqlens, block_table, wor
                                  num_pages, page_size, max_pages, d, scale, causal, dtype, stream)
 
 
+def fa_decode_fp8_workspace_size(B, Hq, Hkv, Nq, d) -> int:
+    return int(lib().fa_decode_fp8_workspace_size(B, Hq, Hkv, Nq, d))
+
+
+def fa_decode_fp8(q, k, v, k_scale, v_scale, o, lse, cache_seqlens, workspace, B, Hq, Hkv, Nq, Nk, d, scale, causal,
+                  dtype, stream) -> int:
+    return lib().fa_decode_fp8(q, k, v, k_scale, v_scale, o, lse, cache_seqlens, workspace, B, Hq, Hkv, Nq, Nk, d,
+                               scale, causal, dtype, stream)
+
+
+def fa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, o, lse, cache_seqlens, block_table, workspace, B, Hq,
+                        Hkv, Nq, num_pages, page_size, max_pages, d, scale, causal, dtype, stream) -> int:
+    return lib().fa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, o, lse, cache_seqlens, block_table,
+                                     workspace, B, Hq, Hkv, Nq, num_pages, page_size, max_pages, d, scale, causal,
+                                     dtype, stream)
+
+
+def fa_build_block_tables(cache_seqlens, new_lens, free_pages, block_table, slot_map, cu_new, new_seqlens, pages_used,
+                          B, num_free, num_pages, page_size, max_pages, total_new, stream) -> int:
+    return lib().fa_build_block_tables(cache_seqlens, new_lens, free_pages, block_table, slot_map, cu_new,
+                                       new_seqlens, pages_used, B, num_free, num_pages, page_size, max_pages,
+                                       total_new, stream)
+
+
+def fa_cache_append_paged(k, v, k_strides, v_strides, k_pages, v_pages, slot_map, total_new, Hkv, num_pages, page_size,
+                          d, dtype, stream) -> int:
+    """*_strides: (token, head) element strides (host), or None for contiguous rows."""
+    return lib().fa_cache_append_paged(k, v, _strides(k_strides), _strides(v_strides), k_pages, v_pages, slot_map,
+                                       total_new, Hkv, num_pages, page_size, d, dtype, stream)
+
+
+def fa_cache_append_fp8(k, v, k_strides, v_strides, k_cache, v_cache, k_scale, v_scale, cu_new, cache_seqlens,
+                        new_seqlens, B, total_new, max_new, Hkv, Nk, d, dtype, stream) -> int:
+    """*_strides: (token, head) element strides (host), or None for contiguous rows."""
+    return lib().fa_cache_append_fp8(k, v, _strides(k_strides), _strides(v_strides), k_cache, v_cache, k_scale,
+                                     v_scale, cu_new, cache_seqlens, new_seqlens, B, total_new, max_new, Hkv, Nk, d,
+                                     dtype, stream)
+
+
+def fa_cache_append_paged_fp8(k, v, k_strides, v_strides, k_pages, v_pages, k_scale, v_scale, cu_new, cache_seqlens,
+                              new_seqlens, block_table, B, total_new, max_new, Hkv, num_pages, page_size, max_pages, d,
+                              dtype, stream) -> int:
+    """*_strides: (token, head) element strides (host), or None for contiguous rows."""
+    return lib().fa_cache_append_paged_fp8(k, v, _strides(k_strides), _strides(v_strides), k_pages, v_pages, k_scale,
+                                           v_scale, cu_new, cache_seqlens, new_seqlens, block_table, B, total_new,
+                                           max_new, Hkv, num_pages, page_size, max_pages, d, dtype, stream)
+
+
 def fa_status_string(s: int) -> str:
     return lib().fa_status_string(s).decode()
 
@@ -458,3 +515,197 @@ def attention_fwd_fp8(q8, k8, v8, q_scale, k_scale, v_scale, scale: float | None
                       o.data_ptr(), L.data_ptr(), B, Hq, Hkv, Nq, Nk, d, float(scale), int(bool(causal)),
                       _stream(stream)), "fa_fwd_fp8")
     return o, L
+
+
+# Serving. These write caches and tables in place, so nothing is copied or converted on the way:
+# every tensor must already have the type and the (contiguous) layout the entry point takes, and all
+# must lie on one device, which need not be the current one. `stream`: as above, a stream of that device.
+def _on(device, fn):
+    """fn() with `device` current."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return fn()
+    with torch.cuda.device(device):
+        return fn()
+
+
+def _own(t, name: str, dtypes, device, shape=None):
+    """`t` as it is, or an error: its type, device, layout and (where given) shape."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(x) for x in dtypes)}, got {t.dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on the CUDA device of the other tensors")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _temporary(make, device, stream):
+    """A buffer of this call alone: kept from other uses until `stream` has run the call."""
+    import torch
+    t = make()
+    if stream is not None:
+        t.record_stream(stream if hasattr(stream, "cuda_stream") else
+                        torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else
+                        torch.cuda.default_stream(device))
+    return t
+
+
+def _rows(t, name: str, device):
+    """(token, head) strides of new rows [T, Hkv, d], any 16-byte multiples; None when contiguous."""
+    if t.dim() != 3 or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be [tokens, Hkv, d] on the CUDA device of the other tensors")
+    if t.is_contiguous():
+        return None
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    # A dimension of one element may carry any stride; it is never stepped over.
+    st = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    sh = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    return (st, sh)
+
+
+def attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens=None, scale: float | None = None,
+                         causal: bool = False, block_table=None, workspace=None, out=None, lse=None, stream=None):
+    """Split-KV decode over an E4M3 cache: q [B,Nq,Hq,d] (bf16 or fp16) against codes (uint8 or float8_e4m3fn).
+
+    Contiguous cache: k/v [B,Nk,Hkv,d], k/v_scale float32 [B,Hkv,ceil(Nk/128)], sequence b using its
+    first cache_seqlens[b] keys (int32; all Nk when None). Paged cache (block_table int32
+    [B,max_pages]): k/v [num_pages,page_size,Hkv,d], k/v_scale [num_pages,Hkv], cache_seqlens
+    required. Returns O [B,Nq,Hq,d] (q's type) and L float32 [B,Hq,Nq]."""
+    import torch
+    dev = q.device
+    codes, f32, i32 = (torch.uint8, torch.float8_e4m3fn), (torch.float32,), (torch.int32,)
+    _own(q, "q", (torch.bfloat16, torch.float16), dev)
+    B, Nq, Hq, d = q.shape
+    n0, n1, Hkv, _ = k_cache.shape
+    paged = block_table is not None
+    _own(k_cache, "k_cache", codes, dev, (n0, n1, Hkv, d) if paged else (B, n1, Hkv, d))
+    _own(v_cache, "v_cache", codes, dev, k_cache.shape)
+    factors = (n0, Hkv) if paged else (B, Hkv, (n1 + 127) // 128)
+    _own(k_scale, "k_scale", f32, dev, factors)
+    _own(v_scale, "v_scale", f32, dev, factors)
+    if cache_seqlens is not None:
+        _own(cache_seqlens, "cache_seqlens", i32, dev, (B,))
+    if paged:
+        if cache_seqlens is None:
+            raise ValueError("a paged cache needs cache_seqlens")
+        _own(block_table, "block_table", i32, dev, (B, block_table.shape[1]))
+    if scale is None:
+        scale = d ** -0.5
+
+    def call():
+        need = max(fa_decode_fp8_workspace_size(B, Hq, Hkv, Nq, d), 16)
+        if workspace is None:
+            ws = _temporary(lambda: torch.empty(need, dtype=torch.uint8, device=dev), dev, stream)
+        else:
+            ws = _own(workspace, "workspace", (torch.uint8,), dev)
+            if ws.numel() < need:
+                raise ValueError(f"workspace must hold {need} bytes, got {ws.numel()}")
+        o = torch.empty_like(q) if out is None else _own(out, "out", (q.dtype,), dev, q.shape)
+        L = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else \
+            _own(lse, "lse", f32, dev, (B, Hq, Nq))
+        sl = 0 if cache_seqlens is None else cache_seqlens.data_ptr()
+        if paged:
+            st = fa_decode_paged_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                     v_scale.data_ptr(), o.data_ptr(), L.data_ptr(), sl, block_table.data_ptr(),
+                                     ws.data_ptr(), B, Hq, Hkv, Nq, n0, n1, block_table.shape[1], d, float(scale),
+                                     int(bool(causal)), _dtype_code(q), _stream(stream))
+            _check(st, "fa_decode_paged_fp8")
+        else:
+            st = fa_decode_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                               v_scale.data_ptr(), o.data_ptr(), L.data_ptr(), sl, ws.data_ptr(), B, Hq, Hkv, Nq, n1,
+                               d, float(scale), int(bool(causal)), _dtype_code(q), _stream(stream))
+            _check(st, "fa_decode_fp8")
+        return o, L
+
+    return _on(dev, call)
+
+
+def build_block_tables(cache_seqlens, new_lens, free_pages, block_table, page_size: int, num_pages: int,
+                       total_new: int, slot_map=None, cu_new=None, new_seqlens=None, pages_used=None, stream=None):
+    """Pages of `free_pages` for every request's new tokens, written into block_table int32 [B,max_pages].
+
+    cache_seqlens int32 [B] (None: every request is new), new_lens int32 [B], free_pages int32
+    [num_free]. Returns slot_map int32 [total_new] (page * page_size + row of every packed new
+    token, -1 for none), cu_new int32 [B+1], new_seqlens int32 [B] and pages_used int32 [1], the
+    number of entries of free_pages taken."""
+    import torch
+    dev, i32 = new_lens.device, (torch.int32,)
+    B = new_lens.shape[0]
+    _own(new_lens, "new_lens", i32, dev, (B,))
+    if cache_seqlens is not None:
+        _own(cache_seqlens, "cache_seqlens", i32, dev, (B,))
+    _own(free_pages, "free_pages", i32, dev, (free_pages.numel(),))
+    _own(block_table, "block_table", i32, dev, (B, block_table.shape[1]))
+
+    def call():
+        res = []
+        for t, name, n in ((slot_map, "slot_map", total_new), (cu_new, "cu_new", B + 1),
+                           (new_seqlens, "new_seqlens", B), (pages_used, "pages_used", 1)):
+            res.append(torch.empty(n, dtype=torch.int32, device=dev) if t is None else _own(t, name, i32, dev, (n,)))
+        st = fa_build_block_tables(0 if cache_seqlens is None else cache_seqlens.data_ptr(), new_lens.data_ptr(),
+                                   free_pages.data_ptr(), block_table.data_ptr(), *[t.data_ptr() for t in res], B,
+                                   free_pages.numel(), int(num_pages), int(page_size), block_table.shape[1],
+                                   int(total_new), _stream(stream))
+        _check(st, "fa_build_block_tables")
+        return tuple(res)
+
+    return _on(dev, call)
+
+
+def cache_append_paged(k_new, v_new, k_pages, v_pages, slot_map, stream=None):
+    """Rows [T,Hkv,d] of k_new and v_new (any 16-byte strides) into the 16-bit page pools
+    [num_pages,page_size,Hkv,d] at slot_map int32 [T]; slots outside the pool are skipped."""
+    import torch
+    dev = k_pages.device
+    ks, vs = _rows(k_new, "k_new", dev), _rows(v_new, "v_new", dev)
+    T, Hkv, d = k_new.shape
+    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new must have one shape and type")
+    n, page = k_pages.shape[:2]
+    _own(k_pages, "k_pages", (k_new.dtype,), dev, (n, page, Hkv, d))
+    _own(v_pages, "v_pages", (k_new.dtype,), dev, (n, page, Hkv, d))
+    _own(slot_map, "slot_map", (torch.int32,), dev, (T,))
+    _check(_on(dev, lambda: fa_cache_append_paged(
+        k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_pages.data_ptr(), v_pages.data_ptr(), slot_map.data_ptr(), T,
+        Hkv, n, page, d, _dtype_code(k_new), _stream(stream))), "fa_cache_append_paged")
+
+
+def cache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cu_new, cache_seqlens, new_seqlens,
+                     max_new: int, block_table=None, stream=None):
+    """Rows [T,Hkv,d] of k_new and v_new (bf16 or fp16, any 16-byte strides) quantised into an E4M3 cache.
+
+    Sequence b's rows cu_new[b].. become its positions cache_seqlens[b] .. new_seqlens[b]-1 (int32
+    tensors, as build_block_tables gives them), at most max_new of them. Caches and factors:
+    the layouts of attention_decode_fp8 (paged with block_table), written in place."""
+    import torch
+    dev = k_cache.device
+    codes, f32, i32 = (torch.uint8, torch.float8_e4m3fn), (torch.float32,), (torch.int32,)
+    ks, vs = _rows(k_new, "k_new", dev), _rows(v_new, "v_new", dev)
+    T, Hkv, d = k_new.shape
+    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new must have one shape and type")
+    B = cache_seqlens.shape[0]
+    n0, n1 = k_cache.shape[:2]
+    paged = block_table is not None
+    _own(k_cache, "k_cache", codes, dev, (n0 if paged else B, n1, Hkv, d))
+    _own(v_cache, "v_cache", codes, dev, k_cache.shape)
+    factors = (n0, Hkv) if paged else (B, Hkv, (n1 + 127) // 128)
+    _own(k_scale, "k_scale", f32, dev, factors)
+    _own(v_scale, "v_scale", f32, dev, factors)
+    _own(cu_new, "cu_new", i32, dev, (B + 1,))
+    _own(cache_seqlens, "cache_seqlens", i32, dev, (B,))
+    _own(new_seqlens, "new_seqlens", i32, dev, (B,))
+    head = (k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), cu_new.data_ptr(), cache_seqlens.data_ptr(), new_seqlens.data_ptr())
+    if paged:
+        _own(block_table, "block_table", i32, dev, (B, block_table.shape[1]))
+        _check(_on(dev, lambda: fa_cache_append_paged_fp8(
+            *head, block_table.data_ptr(), B, T, int(max_new), Hkv, n0, n1, block_table.shape[1], d,
+            _dtype_code(k_new), _stream(stream))), "fa_cache_append_paged_fp8")
+    else:
+        _check(_on(dev, lambda: fa_cache_append_fp8(*head, B, T, int(max_new), Hkv, n1, d, _dtype_code(k_new),
+                                                    _stream(stream))), "fa_cache_append_fp8")

@@ -14,6 +14,7 @@
 
 #include "fa.h"
 #include "bwd_grid.h"
+#include "fa_host.h"
 #include "per_device.h"
 #include "fa_fwd.cuh"
 #include "fa_bwd.cuh"
@@ -926,6 +927,18 @@ fa_status varlen_bwd(const void* q, const void* k, const void* v, const void* o,
 
 }  // namespace
 
+// What the other sources share (fa_host.h).
+namespace fa_host {
+int* error_word() { return ::error_word(); }
+int sm_count() { return ::sm_count(); }
+int current_device() { return ::current_device(); }
+fa_status make_map_box(CUtensorMap* m, const void* base, int d, int H, int64_t rows, int64_t batches, bool bf16,
+                       int64_t sh, int64_t ss, int64_t sb, int box_h, int box_rows, bool promote_256,
+                       int elem_bytes) {
+    return ::make_map_box(m, base, d, H, rows, batches, bf16, sh, ss, sb, box_h, box_rows, promote_256, elem_bytes);
+}
+}  // namespace fa_host
+
 extern "C" {
 
 fa_status fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
@@ -1258,7 +1271,7 @@ fa_status fa_get_last_device_error(fa_stream_t stream) {
     g_last_site = v;
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_fa_error, &zero, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-    if (v == fa::kErrSeqlenBound) return FA_ERR_INVALID_ARG;
+    if (v == fa::kErrSeqlenBound || v == fa::kErrCacheRange) return FA_ERR_INVALID_ARG;
     return (v >= fa::kErrTimeoutBase && v < fa::kErrSmemAlign) ? FA_ERR_TIMEOUT : FA_ERR_CUDA;
 }
 

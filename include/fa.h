@@ -430,6 +430,128 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
                           float scale, int causal, fa_dtype dtype, fa_stream_t stream);
 
 /*
+ * Decode over an 8-bit cache: the attention of fa_decode / fa_decode_paged where keys
+ * and values are held as E4M3 codes with one float32 factor per block of tokens and KV
+ * head (the block scaling of fa_fwd_fp8; "FlashAttention/zh", section "variants", names
+ * FP8 and the paged cache):
+ *     K[j, h, :] = k_scale(block of j, h) * e4m3(k[j, h, :]), and likewise V,
+ * so a cache takes half the bytes of a 16-bit one. The queries keep their 16 bits: a
+ * query is split into E4M3 terms whose sum it is (two for bf16, three for fp16; exact
+ * for values within 2^-13 of the row's largest, else an error of 2^-22 of that), and so
+ * is P (8 significant bits for bf16, 12 for fp16, relative to the key tile's largest
+ * weight), so that both products run on the 8-bit tensor-core path. Sums are fp32.
+ *   q [B,Nq,Hq,d] and o (dtype), lse [B,Hq,Nq] (float32): as fa_decode.
+ *   fa_decode_fp8: k, v [B,Nk,Hkv,d] E4M3 bytes; a block is 128 tokens: k_scale, v_scale
+ *       DEVICE float32 [B,Hkv,ceil(Nk/128)] (the layout of fa_fwd_fp8).
+ *   fa_decode_paged_fp8: k_pages, v_pages [num_pages,page_size,Hkv,d]; a block is a page:
+ *       k_scale, v_scale DEVICE float32 [num_pages,Hkv]. A block_table entry outside
+ *       [0, num_pages) reads zeros.
+ *   The factors must be finite and > 0 where the sequence has tokens (not checked: they
+ *       live on the device), 4-byte aligned; those of blocks past a sequence's length
+ *       are not used. fa_cache_append_fp8 / fa_cache_append_paged_fp8 write both.
+ *   workspace: device buffer of fa_decode_fp8_workspace_size(B,Hq,Hkv,Nq,d) bytes,
+ *       16-byte aligned, owned by the caller (query it with the device the call will run
+ *       on current; 0 when no device is visible).
+ * Every other argument, result and error is that of fa_decode / fa_decode_paged.
+ */
+size_t fa_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
+fa_status fa_decode_fp8(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale,
+                        void* o, float* lse, const int* cache_seqlens, void* workspace,
+                        int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                        float scale, int causal, fa_dtype dtype, fa_stream_t stream);
+fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                              const float* k_scale, const float* v_scale, void* o, float* lse,
+                              const int* cache_seqlens, const int* block_table, void* workspace,
+                              int B, int Hq, int Hkv, int Nq, int num_pages, int page_size, int max_pages, int d,
+                              float scale, int causal, fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * Block tables and slot maps for the next tokens of a batch of requests, built on the
+ * GPU from their lengths (the block table of fa_decode_paged; no host round trip between
+ * decode steps). Request b holds n = cache_seqlens[b] tokens in the pages of its table
+ * row and gets c = new_lens[b] more. The pages it lacks,
+ *     need_b = ceil((n + c) / page_size) - ceil(n / page_size),
+ * come from free_pages in request order: request b takes free_pages[sum of need before
+ * b ..]. New tokens are packed in request order.
+ *   cache_seqlens: DEVICE int32 [B], or NULL (every request is new). new_lens [B].
+ *   free_pages: DEVICE int32 [num_free], page indices nobody holds.
+ *   block_table: DEVICE int32 [B, max_pages], in and out: entries ceil(n/page_size) ..
+ *       ceil((n+c)/page_size)-1 of a row are written, the others left as they were.
+ *   slot_map: DEVICE int32 [total_new]: token t of the packed new tokens goes to row
+ *       slot_map[t] = page * page_size + position % page_size of the page pools; -1 for a
+ *       token that has no place.
+ *   cu_new: DEVICE int32 [B+1], the requests' first packed tokens (a sum past total_new is
+ *       cut there). new_seqlens: DEVICE int32 [B], n + c. It must not be cache_seqlens or
+ *       new_lens itself (FA_ERR_INVALID_ARG).
+ *   pages_used: DEVICE int32 [1]: how many entries of free_pages were taken, from its start.
+ *   A request is served whole or not at all. One that does not fit (c or n < 0; n + c past
+ *   max_pages * page_size; the free list or the total_new slots run out) gets nothing: its
+ *   slots are -1, new_seqlens[b] = n, its table row stays; so does every later request that
+ *   needs pages once the free list has run out. The device error word then makes the
+ *   next fa_get_last_device_error return FA_ERR_INVALID_ARG; so does a page outside
+ *   [0, num_pages) in a request's row, whose tokens get slot -1.
+ *   page_size >= 1; num_pages * page_size and max_pages * page_size below 2^31
+ *   (FA_ERR_UNSUPPORTED). All pointers 4-byte aligned.
+ */
+fa_status fa_build_block_tables(const int* cache_seqlens, const int* new_lens, const int* free_pages,
+                                int* block_table, int* slot_map, int* cu_new, int* new_seqlens, int* pages_used,
+                                int B, int num_free, int num_pages, int page_size, int max_pages, int total_new,
+                                fa_stream_t stream);
+
+/*
+ * New keys and values into the 16-bit page pools of fa_decode_paged: row t of k and v goes
+ * to row slot_map[t] of k_pages and v_pages [num_pages, page_size, Hkv, d] (the slot map of
+ * fa_build_block_tables). A slot outside [0, num_pages * page_size) is skipped. Two tokens
+ * with the same slot leave one of the two rows' values in each 16-byte piece, not
+ * necessarily the same one.
+ *   k, v [total_new, Hkv, d] (dtype); k_strides, v_strides: HOST arrays {token, head} of
+ *       element strides with the rules of fa_varlen_fwd_strided, or NULL (contiguous).
+ *   slot_map: DEVICE int32 [total_new].
+ *   Tensors 16-byte aligned; d is 64 or 128; page_size >= 1;
+ *   num_pages * page_size below 2^31 (FA_ERR_UNSUPPORTED).
+ */
+fa_status fa_cache_append_paged(const void* k, const void* v, const long long* k_strides, const long long* v_strides,
+                                void* k_pages, void* v_pages, const int* slot_map, int total_new, int Hkv,
+                                int num_pages, int page_size, int d, fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * New keys and values quantised into the E4M3 caches of fa_decode_fp8 /
+ * fa_decode_paged_fp8. Sequence b's tokens cu_new[b] .. of the packed k and v become its
+ * positions cache_seqlens[b] .. new_seqlens[b] - 1. For every block and KV head a call
+ * writes to, with the largest finite magnitude a of its new values there,
+ *     f = the smallest power of two with a <= 448 f, at least 2^-100;
+ * a block that held earlier tokens of the sequence (positions below cache_seqlens[b]) keeps
+ * the larger of f and its factor; where it grows, the earlier tokens' codes are rescaled
+ * and rounded to E4M3 again (exact for codes that stay at or above 2^-6). A block whose
+ * first token is new starts afresh: its old factor counts for nothing. The new
+ * codes are the values over the factor rounded to nearest even; infinities and NaN are
+ * stored as NaN. Rows past the new tokens are left as they were.
+ *   k, v, strides: as fa_cache_append_paged. cu_new DEVICE int32 [B+1], cache_seqlens and
+ *       new_seqlens DEVICE int32 [B]: as fa_build_block_tables takes and gives them (a
+ *       request it refused has new_seqlens = cache_seqlens: nothing is written).
+ *   k_cache, v_cache [B,Nk,Hkv,d] with k_scale, v_scale [B,Hkv,ceil(Nk/128)], or page pools
+ *       with [num_pages,Hkv] and block_table [B,max_pages]: in and out. Two
+ *       sequences that append in one call must not do so to the same page.
+ *   max_new: upper bound of one sequence's new tokens (grid sizing).
+ *   A sequence whose lengths do not fit (negative, more than max_new new tokens, past the
+ *   capacity, tokens outside [0, total_new)) is left out, as is a block whose page lies
+ *   outside [0, num_pages); the device error word then makes the next
+ *   fa_get_last_device_error return FA_ERR_INVALID_ARG.
+ *   Tensors 16-byte aligned, factors and integers 4-byte; d is 64 or 128; page_size as
+ *   fa_decode_paged.
+ */
+fa_status fa_cache_append_fp8(const void* k, const void* v, const long long* k_strides, const long long* v_strides,
+                              void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int* cu_new,
+                              const int* cache_seqlens, const int* new_seqlens, int B, int total_new, int max_new,
+                              int Hkv, int Nk, int d, fa_dtype dtype, fa_stream_t stream);
+fa_status fa_cache_append_paged_fp8(const void* k, const void* v, const long long* k_strides,
+                                    const long long* v_strides, void* k_pages, void* v_pages, float* k_scale,
+                                    float* v_scale, const int* cu_new, const int* cache_seqlens,
+                                    const int* new_seqlens, const int* block_table, int B, int total_new,
+                                    int max_new, int Hkv, int num_pages, int page_size, int max_pages, int d,
+                                    fa_dtype dtype, fa_stream_t stream);
+
+/*
  * Backward without a caller-provided workspace. This entry point has no
  * counterpart in the pages; it exists for callers that cannot allocate
  * device memory themselves (a host framework that owns every allocation,
@@ -481,8 +603,8 @@ const char* fa_status_string(fa_status s);
  * word (each GPU has its own; a kernel records into the word of the device it
  * runs on): FA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the
  * last call, FA_ERR_INVALID_ARG if a varlen kernel met a sequence longer than
- * its max_seqlen bound, FA_ERR_CUDA if the synchronisation failed or a kernel
- * refused to run, FA_OK otherwise.
+ * its max_seqlen bound or a serving kernel lengths or pages that do not fit, FA_ERR_CUDA
+ * if the synchronisation failed or a kernel refused to run, FA_OK otherwise.
  */
 fa_status fa_get_last_device_error(fa_stream_t stream);
 
