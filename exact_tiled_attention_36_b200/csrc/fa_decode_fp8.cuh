@@ -1,112 +1,908 @@
 // fa_decode_fp8.cuh: attention of a few query tokens per sequence over an E4M3 key/value
 // cache with one float32 factor per block of tokens and KV head, on sm_100a.
 //
-//     s_j = scale k_f(j) (q . k8_j),  O = sum_j softmax(s)_j v_f(j) v8_j
+//     s_j = scale k_f(j) (q . k8_j),   O = sum_j softmax(s)_j v_f(j) v8_j
+//
+// What bounds it is the cache: 2 d bytes a key and KV head, read once. The codes must
+// therefore go from HBM to the tensor core as they are (expanding them to 16 bits in the
+// SM would cost more shared-memory traffic than the products), while the queries and the
+// weights have 8 or more significant bits that E4M3's four do not hold. Both are split
+// into terms: x = t1 + t2 / 16 (+ t3 / 256) with t1 = e4m3(x), t2 = e4m3(16 (x - t1)), ...
+// Rounding to four significant bits leaves a remainder of four fewer, so two terms hold a
+// bf16 value and three an fp16 value exactly (within E4M3's range: x is scaled by a power
+// of two so that its largest magnitude is below 448). The terms are further rows of the
+// same product, so they cost no further pass over the codes.
+//
+// Products, with keys along the tensor core's M = 128 as in the 16-bit narrow kernel:
+//     S^T = K8 Q^T      (M = 128 keys, N = rows x terms, K = d)
+//     O_t^T = V8^T P^T  (M = d,        N = rows x terms, K = 128 keys)
+// Unlike there, P of a tile is taken relative to the TILE's largest score, and O_t is a
+// product of its own, added to the running output in registers with the factor
+//     f = 2^(m_tile - m_run) v_max(tile) / 256
+// per row: E4M3 spans 2^17, and with a reference that stays at the running maximum the
+// small weights of a long tail behind one large key would all round to zero. This also
+// frees the accumulation from rescaling in TMEM, and block factors of V of any size
+// enter f (the tile's largest) and P (a block's share of it).
+//
+// Work split, segments and merge: as fa_decode.cuh (stream-K over the key tiles of all
+// items laid end to end). An item is (sequence, KV head, chunk of RC query rows). d = 64:
+// an item takes two adjacent KV heads, whose code rows form one 128-byte row; S^T of each
+// is a product over its own 64 bytes, O^T lanes 64 k .. hold head k.
+//
+// Two CTAs share an SM (each 3 key tiles deep), so one's softmax overlaps the other's
+// products and loads. Warp roles (256 threads): warp 0 TMA producer (its lanes issue the
+// boxes of a tile), warp 1 TMEM and the MMA thread, warp 2 block factors, warp 3 the
+// queries' terms, warps 4-7 softmax (thread l: key l of every tile, then d index l of O).
 #pragma once
 
+#include "fa_cache.cuh"
 #include "sm100.cuh"
 
 namespace fa {
 
 struct Decode8Args {
-    const void* q;           // [B, Nq, Hq, d] 16-bit
-    const uint8_t* k;        // [B, Nk, Hkv, d] or [num_pages, page_size, Hkv, d]
-    const uint8_t* v;
+    const uint16_t* q;       // [B, Nq, Hq, d] 16-bit
     const float* k_scale;    // [B, Hkv, per_seq] or [num_pages, Hkv]
     const float* v_scale;
-    void* o;                 // [B, Nq, Hq, d] 16-bit
+    uint16_t* o;             // [B, Nq, Hq, d] 16-bit
     float* lse;              // [B, Hq, Nq]
+    float* o_part;           // [slots, RT, d] normalised partial outputs
+    float* lse_part;         // [slots, RT], log2
+    long long* meta;         // [0] = T, [1 + item] = the item's first unit (lengths given)
     const int* seqlens;      // [B] or null (every sequence has cap keys)
     const int* block_table;  // [B, per_seq]; null: contiguous
-    int B, Hq, Hkv, group, Nq;
-    int cap, unit, per_seq, num_pages;  // keys a sequence can hold, keys of a block, blocks of a sequence
+    int B, Hq, Hkv, group, Nq, R;
+    int cap, per_seq, num_pages;       // keys a sequence can hold, its blocks, pages of the pool
+    int page_size, page_box;           // rows of a page and of one TMA box (contiguous: 128)
+    int HV, nch, RC;         // items of a sequence = heads (or pairs) x chunks of RC rows
+    int G;                   // CTAs of the split kernel
     float scale_log2;
+    int* err;
 };
 
-__device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(byte));
-    return unpack_lo<false>(h);
+constexpr int kDec8Threads = 256;
+constexpr int kDec8Ctas = 2;       // per SM
+constexpr int kDec8ItemCost = 2;   // units of a segment's fixed work (see kDecItemCost)
+
+template <bool BF16, bool PAIR, int RT>
+struct Dec8Cfg {
+    static constexpr int NT = BF16 ? 2 : 3;                       // terms of a query and of a weight
+    static constexpr int N = (NT * RT + 15) / 16 * 16;            // rows of P
+    static constexpr int RH = PAIR ? RT / 2 : RT;                 // rows of one KV head
+    static constexpr int NH = (NT * RH + 15) / 16 * 16;           // rows of Q of one KV head
+    static constexpr int NQ = PAIR ? 2 * NH : NH;
+    static constexpr int kTile = 128 * 128;                       // one K or V tile
+    static constexpr int kUnits = N > 32 ? 5 : 6;                 // ring of tiles: K, V, K, V, ...
+    static constexpr int kQB = N > 16 ? 1 : 2;                    // query buffers
+    static constexpr int kScSlots = 4;                            // tiles of block factors
+    static constexpr int kQOff = 0;
+    static constexpr int kPOff = kQOff + kQB * NQ * 128;
+    static constexpr int kRingOff = kPOff + 2 * N * 128;
+    static constexpr int kBarOff = kRingOff + kUnits * kTile;
+    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 6 + 5;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 112 bytes: dec8_locate
+    static constexpr int kScOff = (kMiscOff + 112 + 15) / 16 * 16;  // float [slots][40]
+    static constexpr int kQfOff = kScOff + kScSlots * 40 * 4;     // float [2][RT]: scale of a query row
+    static constexpr int kRedOff = kQfOff + 2 * RT * 4;           // float [2][4][RT]: warps' maxima
+    static constexpr int kRowOff = kRedOff + 8 * RT * 4;          // float [4][5][RT]: a warp's row values
+    static constexpr int kSumOff = kRowOff + 20 * RT * 4;         // float [4][RT]: warps' sums
+    static constexpr int kSmemBytes = kSumOff + 4 * RT * 4;
+    static constexpr uint32_t kColO = 2 * NQ;                     // S^T buffers at 0 and NQ
+    static constexpr uint32_t kCols = 2 * NQ + 2 * N;
+    static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
+    static_assert(kCols <= 256, "two CTAs share the SM's 512 columns");
+    static_assert(kRingOff % 1024 == 0 && kPOff % 1024 == 0, "swizzle atoms");
+    static_assert(kSmemBytes <= 115712, "two CTAs share the SM's shared memory");
+};
+
+// ------------------------------------------------------------------- work split
+struct Dec8Item {
+    int b, vh, len, ntk, cost;
+    long long P;  // first unit of its cost
+};
+
+__device__ __forceinline__ int dec8_len(const Decode8Args& a, int b) {
+    return a.seqlens ? min(max(a.seqlens[b], 0), a.cap) : a.cap;
 }
 
-// One CTA per query row: its four warps take every fourth key, a lane d / 32 values,
-// each warp with an online softmax of its own; the four are merged at the end.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) fa_decode8_rows_kernel(const Decode8Args a, const int causal) {
-    constexpr int E = D / 32;
-    __shared__ float s_m[4], s_l[4], s_o[4][D];
+__device__ __forceinline__ Dec8Item dec8_item(const Decode8Args& a, int b, int vh, int len, long long P) {
+    Dec8Item it;
+    it.b = b;
+    it.vh = vh;
+    it.len = len;
+    it.ntk = (len + 127) / 128;
+    it.cost = it.ntk > 0 ? it.ntk + kDec8ItemCost : 0;
+    it.P = P;
+    return it;
+}
+
+// The item after `it`; past the last one P = T.
+__device__ __forceinline__ Dec8Item dec8_next(const Decode8Args& a, const Dec8Item& it, long long T) {
+    if (it.vh + 1 < a.HV) return dec8_item(a, it.b, it.vh + 1, it.len, it.P + it.cost);
+    if (it.b + 1 < a.B) return dec8_item(a, it.b + 1, 0, dec8_len(a, it.b + 1), it.P + it.cost);
+    Dec8Item e = it;
+    e.P = T;
+    e.ntk = e.cost = 0;
+    return e;
+}
+
+__device__ __forceinline__ long long dec8_split(int c, long long T, int G) { return (static_cast<long long>(c) * T) / G; }
+
+struct Dec8Range {
+    long long T, lo, hi;
+    Dec8Item first;
+};
+
+// The key tiles [j0, j0 + n) of an item in the CTA's range (false: none).
+__device__ __forceinline__ bool dec8_segment(const Dec8Range& rg, const Dec8Item& it, int& j0, int& n) {
+    const long long r0 = it.P + kDec8ItemCost;
+    const long long lo = max(rg.lo, r0), hi = min(rg.hi, it.P + it.cost);
+    if (lo >= hi) return false;
+    j0 = static_cast<int>(lo - r0);
+    n = static_cast<int>(hi - lo);
+    return true;
+}
+
+// The CTA's range of the T units and the item that holds its first one; called by every
+// thread (it synchronises the CTA). False, for every thread, when the CTA has none.
+__device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc, Dec8Range& rg) {
+    const int cta = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
+    const int warp = warp_id(), lane = lane_id();
+    constexpr int kWarps = kDec8Threads / 32;
+    int b0;
+    long long P0;
+    if (a.seqlens) {
+        int* found = reinterpret_cast<int*>(misc + 8);
+        int* sh_b0 = reinterpret_cast<int*>(misc + 24);
+        long long* sh_P0 = reinterpret_cast<long long*>(misc + 32);
+        long long* ws = reinterpret_cast<long long*>(misc + 40);  // [8] per-warp sums
+        auto units_of = [&](int b) -> long long {
+            if (b >= a.B) return 0;
+            const int ntk = (dec8_len(a, b) + 127) / 128;
+            return ntk > 0 ? static_cast<long long>(a.HV) * (ntk + kDec8ItemCost) : 0;
+        };
+        long long v = 0;
+        for (int b = tid; b < a.B; b += kDec8Threads) v += units_of(b);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if (lane == 0) ws[warp] = v;
+        if (tid == 0) *found = 0;
+        __syncthreads();
+        rg.T = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) rg.T += ws[w];
+        if (cta == 0 && tid == 0) a.meta[0] = rg.T;
+        rg.lo = dec8_split(cta, rg.T, a.G);
+        rg.hi = dec8_split(cta + 1, rg.T, a.G);
+        if (rg.lo >= rg.hi) return false;
+        __syncthreads();  // every thread has read ws
+        long long run = 0;
+        for (int base = 0; base < a.B; base += kDec8Threads) {
+            const int b = base + tid;
+            const long long x = units_of(b);
+            long long incl = x;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+            }
+            if (lane == 31) ws[warp] = incl;
+            __syncthreads();
+            long long before = 0, total = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const long long y = ws[w];
+                if (w < warp) before += y;
+                total += y;
+            }
+            const long long excl = run + before + incl - x;
+            if (x > 0 && excl <= rg.lo && rg.lo < excl + x) {  // one thread at most
+                *sh_b0 = b;
+                *sh_P0 = excl;
+                *found = 1;
+            }
+            __syncthreads();
+            if (*found) break;
+            run += total;
+        }
+        if (!*found) return false;  // cannot happen: lo < T
+        b0 = *sh_b0;
+        P0 = *sh_P0;
+    } else {
+        const int ntk = (a.cap + 127) / 128;
+        const long long per_b = ntk > 0 ? static_cast<long long>(a.HV) * (ntk + kDec8ItemCost) : 0;
+        rg.T = per_b * a.B;
+        rg.lo = dec8_split(cta, rg.T, a.G);
+        rg.hi = dec8_split(cta + 1, rg.T, a.G);
+        if (rg.lo >= rg.hi) return false;
+        b0 = static_cast<int>(rg.lo / per_b);
+        P0 = b0 * per_b;
+    }
+    const int len = dec8_len(a, b0);
+    const int cost = (len + 127) / 128 + kDec8ItemCost;
+    const int vh = static_cast<int>((rg.lo - P0) / cost);
+    rg.first = dec8_item(a, b0, vh, len, P0 + static_cast<long long>(vh) * cost);
+    return true;
+}
+
+// ------------------------------------------------------------------- primitives
+// N columns of this thread's TMEM lane. The values may be used after tmem_ld_done and a
+// tie (which keeps the compiler from moving their uses above it).
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t addr, uint32_t* r) {
+    if constexpr (N == 2) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+    } else if constexpr (N == 4) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr)
+                     : "memory");
+    } else if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : FA_R8(r, 0)
+                     : "r"(addr)
+                     : "memory");
+    } else {
+        static_assert(N == 16, "columns of one load");
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : FA_R8(r, 0), FA_R8(r, 8)
+            : "r"(addr)
+            : "memory");
+    }
+}
+__device__ __forceinline__ void tmem_ld_done() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void tie(uint32_t* r) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+
+// Largest value over the warp (NaN counts only where every lane has it).
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// A pair of fp16 values as a pair of E4M3 codes (low half: low byte) and back (exact).
+__device__ __forceinline__ uint32_t e4m3x2_of_h2(uint32_t h) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+    return c;
+}
+__device__ __forceinline__ uint32_t h2_of_e4m3x2(uint32_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+    return h;
+}
+// 16 (x - t) of a pair: exact, t being x rounded to E4M3.
+__device__ __forceinline__ uint32_t h2_rest(uint32_t x, uint32_t t) {
+    uint32_t d, r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(t));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(0x4c004c00u));
+    return r;
+}
+// The NT terms of a pair of values (fp16), each a pair of codes.
+template <int NT>
+__device__ __forceinline__ void e4m3_terms(uint32_t x, uint32_t (&c)[NT]) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        c[i] = e4m3x2_of_h2(x);
+        if (i + 1 < NT) x = h2_rest(x, h2_of_e4m3x2(c[i]));
+    }
+}
+
+// ------------------------------------------------------------------- split kernel
+template <bool BF16, bool PAIR, bool PAGED, int RT>
+__global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
+    fa_decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const Decode8Args args, const int causal) {
+    using C = Dec8Cfg<BF16, PAIR, RT>;
+    constexpr int NT = C::NT, U = C::kUnits, QB = C::kQB, SC = C::kScSlots, RH = C::RH;
+    constexpr int D = PAIR ? 64 : 128;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (!smem_base_ok(smem, args.err)) return;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int cta = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
+    const int warp = warp_id(), lane = lane_id();
+    uint8_t* misc = smem + C::kMiscOff;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
+    int* abort_flag = reinterpret_cast<int*>(misc + 4);
+    Dec8Range rg;
+    if (!dec8_locate(args, misc, rg)) return;
+
+    uint8_t* sQ = smem + C::kQOff;
+    uint8_t* sP = smem + C::kPOff;
+    uint8_t* ring = smem + C::kRingOff;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [U] tiles, unit 2 g: K of tile g, 2 g + 1: V
+    uint64_t* empty = full + U;
+    uint64_t* q_full = empty + U;      // [QB] a segment's queries
+    uint64_t* q_empty = q_full + QB;
+    uint64_t* sc_full = q_empty + QB;  // [SC] a tile's block factors
+    uint64_t* sc_empty = sc_full + SC;
+    uint64_t* s_full = sc_empty + SC;  // [2] S^T of tile g in buffer g & 1
+    uint64_t* p_full = s_full + 2;     // [2] P of the tile written, S^T read, O_t of tile g - 2 read
+    uint64_t* pv_done = p_full + 2;    // [2] O_t of the tile complete
+    uint64_t* mma_done = pv_done + 2;
+    uint64_t* sm_done = mma_done + 1;
+    uint64_t* meet_bar = sm_done + 1;  // [2] softmax warps, per tile parity
+    uint64_t* sum_bar = meet_bar + 2;  // once per segment
+    float* sc = reinterpret_cast<float*>(smem + C::kScOff);
+    float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
+
+    // Rows of P past the terms are zeros (those of Q are never looked at: their columns
+    // of S^T are not read, but they must hold codes that are there).
+    for (int i = tid; i < (C::kRingOff - C::kQOff) / 16; i += kDec8Threads)
+        reinterpret_cast<uint4*>(smem + C::kQOff)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (tid == 0) {
+        for (int i = 0; i < U; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < QB; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 5);  // the last S^T product, and each softmax warp's last use of the scales
+        }
+        for (int i = 0; i < SC; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&pv_done[i], 1);
+            mbar_init(&meet_bar[i], 4);
+        }
+        mbar_init(sum_bar, 4);
+        mbar_init(mma_done, 1);
+        mbar_init(sm_done, 128);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+    const WaitCtx wc{abort_flag, args.err};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        // Lane x issues box x of every tile: rows x * page_box .. of the 128 keys, from the
+        // page that holds them (a page outside the pool: zeros). Boxes past the sequence's
+        // end are not loaded.
+        const int pb = args.page_box;
+        int u = 0;
+        bool ok = true;
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+            if (lane == 0 && args.seqlens && it.cost > 0 && it.P >= rg.lo)  // the item starts in this CTA's range
+                args.meta[1 + static_cast<size_t>(it.b) * args.HV + it.vh] = it.P;
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            const int x0 = (it.vh / args.nch) * 128;  // the head's (or pair's) first byte of a row
+            const int* bt = PAGED ? args.block_table + static_cast<size_t>(it.b) * args.per_seq : nullptr;
+            auto page_of = [&](int kt) {
+                const int key = kt * 128 + lane * pb;
+                return PAGED && lane * pb < 128 && key < it.len ? bt[key / args.page_size] : 0;
+            };
+            int page = page_of(j0);
+            for (int j = 0; ok && j < n; ++j) {
+                const int kt = j0 + j;
+                const int boxes = PAGED ? (min(128, it.len - kt * 128) + pb - 1) / pb : 1;
+                const int next = j + 1 < n ? page_of(kt + 1) : 0;  // in flight while this tile's buffers come free
+                for (int kv = 0; kv < 2; ++kv, ++u) {
+                    const int st = u % U;
+                    if (!(ok = warp_all(mbar_wait(&empty[st], ((u / U) & 1) ^ 1u, wc, 120)))) break;
+                    uint8_t* dst = ring + st * C::kTile;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(PAGED ? boxes * pb * 128 : C::kTile));
+                    __syncwarp();
+                    const CUtensorMap* m = kv ? &tm_v : &tm_k;
+                    if (PAGED) {
+                        if (lane < boxes)
+                            tma_load_4d(dst + lane * pb * 128, m, &full[st], x0, (kt * 128 + lane * pb) % args.page_size, page, 0);
+                    } else if (lane == 0) {
+                        tma_load_4d(dst, m, &full[st], x0, kt * 128, it.b, 0);
+                    }
+                }
+                page = next;
+            }
+        }
+        // Leave no load in flight: wait for the last one issued into every buffer.
+        for (int st = 0; st < U && st < u; ++st) mbar_wait_drain(&full[st], ((u - 1 - st) / U) & 1);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_e4m3(128, C::NH, false, false);
+            constexpr uint32_t id_pv = idesc_e4m3(128, C::N, true, false);
+            uint32_t q_addr = smem_u32(sQ);
+            auto issue_s = [&](int gg) {
+                const uint32_t k_addr = smem_u32(ring + ((2 * gg) % U) * C::kTile);
+                const uint32_t d_col = tmem + static_cast<uint32_t>((gg & 1) * C::NQ);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int hd = PAIR ? kk >> 1 : 0;  // d = 64: head hd's 64 bytes are two steps
+                    mma_ss_f8(d_col + hd * C::NH, sdesc_sw128(k_addr + kk * 32, 16, 1024),
+                              sdesc_sw128(q_addr + hd * C::NH * 128 + kk * 32, 16, 1024), id_s,
+                              (PAIR ? kk & 1 : kk) > 0 ? 1u : 0u);
+                }
+                tc_commit(&s_full[gg & 1]);
+                tc_commit(&empty[(2 * gg) % U]);
+            };
+            int gk = 0, nq = 0;
+            bool ok = true;
+            for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+                int j0, n;
+                if (!dec8_segment(rg, it, j0, n)) continue;
+                const int qb = nq % QB;
+                q_addr = smem_u32(sQ + qb * C::NQ * 128);
+                if (!(ok = mbar_wait(&q_full[qb], (nq / QB) & 1, wc, 121))) break;
+                for (int j = 0; ok && j < min(n, 2); ++j) {
+                    const int gg = gk + j;
+                    if (!(ok = mbar_wait(&full[(2 * gg) % U], ((2 * gg) / U) & 1, wc, 122))) break;
+                    tc_fence_after();
+                    issue_s(gg);
+                }
+                if (!ok) break;
+                if (n <= 2) tc_commit(&q_empty[qb]);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int gg = gk + j, b = gg & 1, uv = 2 * gg + 1;
+                    if (!(ok = mbar_wait(&full[uv % U], (uv / U) & 1, wc, 123))) break;
+                    if (!(ok = mbar_wait(&p_full[b], (gg >> 1) & 1, wc, 124))) break;
+                    tc_fence_after();
+                    const uint32_t v_addr = smem_u32(ring + (uv % U) * C::kTile);
+                    const uint32_t p_addr = smem_u32(sP + b * C::N * 128);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss_f8(tmem + C::kColO + static_cast<uint32_t>(b * C::N), sdesc_sw128(v_addr + kk * 4096, C::kTile, 1024),
+                                  sdesc_sw128(p_addr + kk * 32, 16, 1024), id_pv, kk > 0 ? 1u : 0u);
+                    tc_commit(&pv_done[b]);
+                    tc_commit(&empty[uv % U]);
+                    if (j + 2 < n) {  // S^T of tile gg + 2 into the buffer that p_full says was read
+                        const int u2 = 2 * (gg + 2);
+                        if (!(ok = mbar_wait(&full[u2 % U], (u2 / U) & 1, wc, 125))) break;
+                        tc_fence_after();
+                        issue_s(gg + 2);
+                        if (j + 3 == n) tc_commit(&q_empty[qb]);
+                    }
+                }
+                gk += n;
+                ++nq;
+            }
+            tc_commit(mma_done);
+            mbar_wait_drain(mma_done, 0);
+            const uint32_t a = smem_u32(sm_done);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < 4000000000ull) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ block factors
+        // Lane x + 8 kv + 16 h: box x of a tile, key or value factor, head h of the pair. A
+        // slot holds 16 key factors [h][box], 16 value shares 256 v / v_max and v_max / 256 [h].
+        const int x = lane & 7, kv = (lane >> 3) & 1, h = lane >> 4;
+        const int pb = args.page_box;
+        int gk = 0;
+        bool ok = true;
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            const int hh = it.vh / args.nch;
+            const int head = PAIR ? 2 * hh + h : hh;
+            const bool mine = (PAIR || h == 0) && head < args.Hkv;
+            const float* f = kv ? args.v_scale : args.k_scale;
+            auto read = [&](int kt) -> float {
+                const int key = kt * 128 + x * pb;
+                if (!mine || x * pb >= 128 || key >= it.len) return 0.f;
+                if constexpr (PAGED) {
+                    const int pg = args.block_table[static_cast<size_t>(it.b) * args.per_seq + key / args.page_size];
+                    return pg >= 0 && pg < args.num_pages ? f[static_cast<size_t>(pg) * args.Hkv + head] : 0.f;
+                } else {
+                    return f[(static_cast<size_t>(it.b) * args.Hkv + head) * args.per_seq + kt];
+                }
+            };
+            float v = read(j0);
+            for (int j = 0; j < n; ++j) {
+                const int gg = gk + j, slot = gg % SC;
+                const float next = j + 1 < n ? read(j0 + j + 1) : 0.f;
+                float top = v;
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                if (!(ok = warp_all(mbar_wait(&sc_empty[slot], ((gg / SC) & 1) ^ 1u, wc, 126)))) break;
+                float* s = sc + slot * 40;
+                s[kv * 16 + h * 8 + x] = kv ? (top > 0.f ? v / top * 256.f : 0.f) : v;
+                if (kv == 1 && x == 0) s[32 + h] = top * (1.f / 256.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_full[slot]);
+                v = next;
+            }
+            gk += n;
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ query terms
+        int nq = 0;
+        bool ok = true;
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            const int hh = it.vh / args.nch, ch = it.vh % args.nch;
+            const int cols = PAIR ? lane >> 4 : 0;  // the head whose 64 values this lane's columns hold
+            uint2 raw[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const int hd = PAIR ? r / RH : 0;
+                const int gr = ch * args.RC + (PAIR ? r % RH : r);
+                const int head = PAIR ? 2 * hh + hd : hh;
+                raw[r] = make_uint2(0, 0);
+                if (gr < args.R && (PAIR ? r % RH : r) < args.RC && head < args.Hkv && cols == hd) {
+                    const size_t row = (static_cast<size_t>(it.b) * args.Nq + gr / args.group) * args.Hq +
+                                       static_cast<size_t>(head) * args.group + gr % args.group;
+                    raw[r] = *reinterpret_cast<const uint2*>(args.q + row * D + (PAIR ? (lane & 15) : lane) * 4);
+                }
+            }
+            const int qb = nq % QB;
+            if (!(ok = warp_all(mbar_wait(&q_empty[qb], ((nq / QB) & 1) ^ 1u, wc, 127)))) break;
+            uint8_t* dst = sQ + qb * C::NQ * 128;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const int hd = PAIR ? r / RH : 0, rr = PAIR ? r % RH : r;
+                float v[4] = {unpack_lo<BF16>(raw[r].x), unpack_hi<BF16>(raw[r].x), unpack_lo<BF16>(raw[r].y),
+                              unpack_hi<BF16>(raw[r].y)};
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f);
+                const int e = e4m3_exponent(warp_max(top));
+                const float inv = exp2_int(-e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] * inv : __uint_as_float(0x7fffffffu);
+                uint32_t c0[NT], c1[NT];
+                e4m3_terms<NT>(pack2<false>(v[0], v[1]), c0);
+                e4m3_terms<NT>(pack2<false>(v[2], v[3]), c1);
+                if (!PAIR || cols == hd) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const int row = hd * C::NH + t * RH + rr;
+                        *reinterpret_cast<uint32_t*>(dst + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) =
+                            c0[t] | (c1[t] << 16);
+                    }
+                }
+                if (lane == 0) qf[(nq & 1) * RT + r] = args.scale_log2 * exp2_int(e);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[qb]);
+            ++nq;
+        }
+    } else {
+        // ------------------------------------------------------------ softmax, output
+        const int w4 = warp - 4;
+        const int l_idx = w4 * 32 + lane;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+        float* red = reinterpret_cast<float*>(smem + C::kRedOff);  // [2][4][RT]
+        float* row_m = reinterpret_cast<float*>(smem + C::kRowOff) + w4 * 5 * RT;  // this warp's copies of row values
+        float* row_f = row_m + RT;      // [2]: 2^(m_tile - m_run), times the tile's V factor from the second use on
+        float* row_a = row_f + 2 * RT;  // 2^(m_run before - m_run)
+        int* row_hi = reinterpret_cast<int*>(row_a + RT);  // keys a row sees
+        const int box = l_idx / args.page_box;
+        // Row `lane` of the tile: its head of the pair, its query token.
+        const int my_hd = PAIR ? lane / RH : 0, my_rr = PAIR ? lane % RH : lane;
+        float* sums = reinterpret_cast<float*>(smem + C::kSumOff);  // [4][RT], once per segment
+        int gk = 0, nq = 0;
+        bool ok = true;
+        auto meet = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            return warp_all(mbar_wait(bar, parity, wc, site));
+        };
+        auto rows4 = [](const float* p, int r) { return *reinterpret_cast<const float4*>(p + r); };
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            const int hh = it.vh / args.nch, ch = it.vh % args.nch;
+            const int my_gr = ch * args.RC + my_rr;  // this lane's row in its head's group
+            __syncwarp();
+            if (lane < RT) row_hi[lane] = causal ? min(it.len, my_gr / args.group + it.len - args.Nq + 1) : it.len;
+            __syncwarp();
+            const int all_hi = causal ? it.len - args.Nq + 1 : it.len;  // keys below it are seen by every row
+            ok = warp_all(mbar_wait(&q_full[nq % QB], (nq / QB) & 1, wc, 128));
+            if (!ok) break;
+            const float* my_qf = qf + (nq & 1) * RT;
+            float acc[RT], l[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[r] = l[r] = 0.f;
+            float m_run = -INFINITY;  // of row `lane`
+            // acc += f O_t of tile gg, whose factors sit in row_f of its parity.
+            auto drain = [&](int gg) -> bool {
+                const int b = gg & 1;
+                if (!warp_all(mbar_wait(&pv_done[b], (gg >> 1) & 1, wc, 129))) return false;
+                tc_fence_after();
+                uint32_t o[NT][RT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    tmem_ldn<RT>(lane_base + C::kColO + static_cast<uint32_t>(b * C::N + t * RT), o[t]);
+                tmem_ld_done();
+#pragma unroll
+                for (int t = 0; t < NT; ++t) tie<RT>(o[t]);
+#pragma unroll
+                for (int r = 0; r < RT; r += 4) {
+                    const float4 f4 = rows4(row_f + b * RT, r);
+                    const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = __uint_as_float(o[NT - 1][r + i]);
+#pragma unroll
+                        for (int t = NT - 2; t >= 0; --t) v = fmaf(v, 0.0625f, __uint_as_float(o[t][r + i]));
+                        acc[r + i] = fmaf(v, f[i], acc[r + i]);
+                    }
+                }
+                return true;
+            };
+            for (int j = 0; j < n; ++j) {
+                const int gg = gk + j, par = gg & 1, slot = gg % SC;
+                ok = warp_all(mbar_wait(&sc_full[slot], (gg / SC) & 1, wc, 130));
+                if (!ok) break;
+                const float* s_sc = sc + slot * 40;
+                const float kf0 = s_sc[box], kf1 = PAIR ? s_sc[8 + box] : 0.f;
+                const float vs0 = s_sc[16 + box], vs1 = PAIR ? s_sc[24 + box] : 0.f;
+                const float my_vm = s_sc[32 + (lane < RT ? my_hd : 0)];
+                ok = warp_all(mbar_wait(&s_full[par], (gg >> 1) & 1, wc, 131));
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_empty[slot]);
+                tc_fence_after();
+                float x[RT];
+                {
+                    uint32_t s[NT][RT];
+                    const uint32_t s_addr = lane_base + static_cast<uint32_t>(par * C::NQ);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        tmem_ldn<RH>(s_addr + t * RH, s[t]);
+                        if constexpr (PAIR) tmem_ldn<RH>(s_addr + C::NH + t * RH, s[t] + RH);
+                    }
+                    tmem_ld_done();
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) tie<RT>(s[t]);
+#pragma unroll
+                    for (int r = 0; r < RT; r += 4) {
+                        const float4 f4 = rows4(my_qf, r);
+                        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float v = __uint_as_float(s[NT - 1][r + i]);
+#pragma unroll
+                            for (int t = NT - 2; t >= 0; --t) v = fmaf(v, 0.0625f, __uint_as_float(s[t][r + i]));
+                            x[r + i] = v * f[i] * (PAIR && r + i >= RH ? kf1 : kf0);
+                        }
+                    }
+                }
+                if (j == n - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&q_empty[nq % QB]);
+                }
+                const int key = (j0 + j) * 128 + l_idx;
+                if ((j0 + j + 1) * 128 > all_hi) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        if (key >= row_hi[r]) x[r] = -INFINITY;
+                }
+                // Every row's largest score of the tile: over the warp, then the four warps.
+                float* rd = red + par * 4 * RT;
+#pragma unroll
+                for (int r = 0; r < RT; r += 4) {
+                    const float4 v = make_float4(warp_max(x[r]), warp_max(x[r + 1]), warp_max(x[r + 2]), warp_max(x[r + 3]));
+                    if (lane == 0) *reinterpret_cast<float4*>(rd + w4 * RT + r) = v;
+                }
+                ok = meet(&meet_bar[par], (gg >> 1) & 1, 132);
+                if (!ok) break;
+                // Lane r takes row r's running values.
+                bool moved = false;
+                if (lane < RT) {
+                    const float mt = fmaxf(fmaxf(rd[lane], rd[RT + lane]), fmaxf(rd[2 * RT + lane], rd[3 * RT + lane]));
+                    float alpha = 1.f;
+                    if (mt > m_run + kRescaleThreshold) {
+                        alpha = ex2_approx(m_run - mt);  // 0 for the first keys
+                        m_run = mt;
+                        moved = true;
+                    }
+                    const bool none = mt == -INFINITY;
+                    const float f = none ? 0.f : ex2_approx(mt - m_run);
+                    row_m[lane] = none ? 0.f : -mt;
+                    row_f[par * RT + lane] = f;
+                    row_a[lane] = alpha;
+                }
+                moved = __any_sync(0xffffffffu, moved);
+                __syncwarp();
+                // P = 2^(x - m_tile), its sum in the running scale, and its terms times V's share.
+                uint8_t* pb = sP + par * C::N * 128;
+#pragma unroll
+                for (int r = 0; r < RT; r += 4) {
+                    const float4 m4 = rows4(row_m, r), f4 = rows4(row_f + par * RT, r);
+                    const float mm[4] = {m4.x, m4.y, m4.z, m4.w}, ff[4] = {f4.x, f4.y, f4.z, f4.w};
+                    if (moved) {
+                        const float4 a4 = rows4(row_a, r);
+                        l[r] *= a4.x;
+                        l[r + 1] *= a4.y;
+                        l[r + 2] *= a4.z;
+                        l[r + 3] *= a4.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        const float p0 = ex2_approx(x[r + i] + mm[i]), p1 = ex2_approx(x[r + i + 1] + mm[i + 1]);
+                        l[r + i] = fmaf(p0, ff[i], l[r + i]);
+                        l[r + i + 1] = fmaf(p1, ff[i + 1], l[r + i + 1]);
+                        uint32_t c[NT];
+                        e4m3_terms<NT>(pack2<false>(p0 * (PAIR && r + i >= RH ? vs1 : vs0),
+                                                    p1 * (PAIR && r + i + 1 >= RH ? vs1 : vs0)), c);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const int n0 = t * RT + r + i;
+                            pb[n0 * 128 + (((l_idx >> 4) ^ (n0 & 7)) << 4) + (l_idx & 15)] = static_cast<uint8_t>(c[t]);
+                            pb[(n0 + 1) * 128 + (((l_idx >> 4) ^ ((n0 + 1) & 7)) << 4) + (l_idx & 15)] =
+                                static_cast<uint8_t>(c[t] >> 8);
+                        }
+                    }
+                }
+                // The sequence's last tile: rows of V past its end may hold anything (0 x NaN
+                // would reach O); they are zeroed before the product reads them.
+                if (j0 + j == it.ntk - 1 && (it.len & 127) != 0) {
+                    const int uv = 2 * gg + 1;
+                    ok = warp_all(mbar_wait(&full[uv % U], (uv / U) & 1, wc, 133));
+                    if (!ok) break;
+                    const int v0 = it.len & 127;
+                    uint4* vt = reinterpret_cast<uint4*>(ring + (uv % U) * C::kTile + v0 * 128);
+                    for (int i = l_idx; i < (128 - v0) * 8; i += 128) vt[i] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(&p_full[par]);
+                // While this tile's product runs: the previous one's output.
+                if (j > 0 && !(ok = drain(gg - 1))) break;
+                if (moved) {
+#pragma unroll
+                    for (int r = 0; r < RT; r += 4) {
+                        const float4 a4 = rows4(row_a, r);
+                        acc[r] *= a4.x;
+                        acc[r + 1] *= a4.y;
+                        acc[r + 2] *= a4.z;
+                        acc[r + 3] *= a4.w;
+                    }
+                }
+                // The factor of O_t carries the tile's V factor too.
+                __syncwarp();
+                if (lane < RT) row_f[par * RT + lane] *= my_vm;
+                __syncwarp();
+            }
+            if (!ok) break;
+            ok = drain(gk + n - 1);
+            if (!ok) break;
+            // Row sums over the 128 keys' threads (written again a segment later, after
+            // every warp has met at a tile in between).
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                float a = l[r];
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+                if (lane == 0) sums[w4 * RT + r] = a;
+            }
+            if (lane < RT) row_m[lane] = m_run;
+            ok = meet(sum_bar, nq & 1, 134);
+            if (!ok) break;
+            const size_t slot = static_cast<size_t>(cta) + static_cast<size_t>(it.b) * args.HV + it.vh;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const int hd = PAIR ? r / RH : 0, rr = PAIR ? r % RH : r;
+                const int head = PAIR ? 2 * hh + hd : hh;
+                if (rr < args.RC && ch * args.RC + rr < args.R && head < args.Hkv) {
+                    const float lt = sums[r] + sums[RT + r] + sums[2 * RT + r] + sums[3 * RT + r];
+                    // no key: 0; NaN stays NaN
+                    const float v = lt == 0.f ? 0.f : acc[r] / lt;
+                    if (!PAIR || (l_idx >> 6) == hd) args.o_part[(slot * RT + r) * D + (PAIR ? l_idx & 63 : l_idx)] = v;
+                    if (l_idx == r) args.lse_part[slot * RT + r] = lt == 0.f ? -INFINITY : row_m[r] + log2f(lt);
+                }
+            }
+            gk += n;
+            ++nq;
+        }
+        tc_fence_before();
+        mbar_arrive(sm_done);
+    }
+}
+
+// Merge of the segments of each output row: one block of four warps per row of
+// [B, Nq, Hq] (warp w takes every fourth segment, a lane four values).
+template <int D, bool BF16, int RT>
+__global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr bool PAIR = D == 64;
+    constexpr int RH = PAIR ? RT / 2 : RT;
+    __shared__ float4 part[4][D / 4];
     const int lane = lane_id(), warp = warp_id();
     const int h = static_cast<int>(blockIdx.x % a.Hq);
     const int t = static_cast<int>(blockIdx.x / a.Hq % a.Nq), b = static_cast<int>(blockIdx.x / a.Hq / a.Nq);
-    const int hk = h / a.group;
-    const int len = a.seqlens ? min(max(a.seqlens[b], 0), a.cap) : a.cap;
-    const int hi = causal ? min(len, t + len - a.Nq + 1) : len;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((static_cast<size_t>(b) * a.Nq + t) * a.Hq + h) * D + lane * E;
-    float qv[E], acc[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        qv[i] = unpack_lo<BF16>(q[i]);
-        acc[i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int j = warp; j < hi; j += 4) {
-        const int blk = j / a.unit;
-        size_t row;
-        float kf = 0.f, vf = 0.f;
-        bool in = true;
-        if (a.block_table) {
-            const int pg = a.block_table[static_cast<size_t>(b) * a.per_seq + blk];
-            in = pg >= 0 && pg < a.num_pages;  // a page outside the pool reads zeros
-            row = static_cast<size_t>(in ? pg : 0) * a.unit + j % a.unit;
-            if (in) {
-                kf = a.k_scale[static_cast<size_t>(pg) * a.Hkv + hk];
-                vf = a.v_scale[static_cast<size_t>(pg) * a.Hkv + hk];
-            }
+    const int hk = h / a.group, gr = t * a.group + h % a.group;
+    const int vh = (PAIR ? hk / 2 : hk) * a.nch + gr / a.RC;
+    const int r = (PAIR ? hk % 2 * RH : 0) + gr % a.RC;
+    const size_t item = static_cast<size_t>(b) * a.HV + vh;
+    const int len = dec8_len(a, b);
+    const int ntk = (len + 127) / 128;
+    long long T = 0, P = 0;
+    if (ntk > 0) {
+        if (a.seqlens) {
+            T = a.meta[0];
+            P = a.meta[1 + item];
         } else {
-            row = static_cast<size_t>(b) * a.cap + j;
-            const size_t f = (static_cast<size_t>(b) * a.Hkv + hk) * a.per_seq + blk;
-            kf = a.k_scale[f];
-            vf = a.v_scale[f];
+            T = static_cast<long long>(a.B) * a.HV * (ntk + kDec8ItemCost);
+            P = static_cast<long long>(item) * (ntk + kDec8ItemCost);
         }
-        const size_t at = (row * a.Hkv + hk) * D + lane * E;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) s += in ? qv[i] * e4m3_to_float(a.k[at + i]) : 0.f;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= a.scale_log2 * kf;
-        const float m_new = fmaxf(m, s);
-        const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
-        const float p = ex2_approx(s - m_new);
-        m = m_new;
-        l = l * alpha + p;
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = acc[i] * alpha + (in ? p * vf * e4m3_to_float(a.v[at + i]) : 0.f);
     }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+    // The CTAs whose range holds one of the item's tiles: the largest c with
+    // floor(c T / G) <= t, for its first and its last tile.
+    int c0 = 0, c1 = -1;
+    if (ntk > 0 && T > 0) {
+        c0 = static_cast<int>(((P + kDec8ItemCost + 1) * a.G - 1) / T);
+        c1 = static_cast<int>(((P + kDec8ItemCost + ntk) * a.G - 1) / T);
     }
+    const bool all_have = T >= a.G;
+    auto has = [&](int c) { return all_have || dec8_split(c, T, a.G) < dec8_split(c + 1, T, a.G); };
+    auto at = [&](int c) { return (static_cast<size_t>(c) + item) * RT + r; };
+    float Lm = -INFINITY;
+    bool nan = false;
+    for (int c = c0 + lane; c <= c1; c += 32)
+        if (has(c)) {
+            const float L = a.lse_part[at(c)];
+            Lm = fmaxf(Lm, L);
+            nan |= L != L;
+        }
+    Lm = warp_max(Lm);
+    nan = __any_sync(0xffffffffu, nan);
+    const float ref = Lm == -INFINITY ? 0.f : Lm;
+    float wsum = 0.f;
+    for (int c = c0 + lane; c <= c1; c += 32)
+        if (has(c)) wsum += ex2_approx(a.lse_part[at(c)] - ref);
 #pragma unroll
-    for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = acc[i];
+    for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane < D / 4) {
+#pragma unroll 2
+        for (int c = c0 + warp; c <= c1; c += 4) {
+            if (!has(c)) continue;
+            const float w = ex2_approx(a.lse_part[at(c)] - ref);
+            const float4 x = reinterpret_cast<const float4*>(a.o_part + at(c) * D)[lane];
+            acc.x = fmaf(w, x.x, acc.x);
+            acc.y = fmaf(w, x.y, acc.y);
+            acc.z = fmaf(w, x.z, acc.z);
+            acc.w = fmaf(w, x.w, acc.w);
+        }
+        part[warp][lane] = acc;
+    }
     __syncthreads();
-    const float mx = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    float w[4], lt = 0.f;
+    if (warp != 0 || lane >= D / 4) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = s_m[i] == -INFINITY ? 0.f : ex2_approx(s_m[i] - mx);
-        lt += w[i] * s_l[i];
+    for (int w = 1; w < 4; ++w) {
+        const float4 y = part[w][lane];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
     }
-    const int c = static_cast<int>(threadIdx.x);
-    if (c < D) {
-        float x = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x += w[i] * s_o[i][c];
-        const uint32_t u = pack2<BF16>(lt > 0.f ? x / lt : (lt == 0.f ? 0.f : lt), 0.f);
-        static_cast<uint16_t*>(a.o)[((static_cast<size_t>(b) * a.Nq + t) * a.Hq + h) * D + c] =
-            static_cast<uint16_t>(u & 0xffffu);
-    }
-    if (c == 0) a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Nq + t] = lt == 0.f ? -INFINITY : (mx + log2f(lt)) * kLn2;
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    uint16_t* o = a.o + static_cast<size_t>(blockIdx.x) * D + lane * 4;
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+    if (lane == 0)
+        a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Nq + t] =
+            nan ? __uint_as_float(0x7fffffffu) : (wsum == 0.f ? -INFINITY : (Lm + log2f(wsum)) * kLn2);
 }
 
 }  // namespace fa

@@ -104,6 +104,92 @@ fa_status append8(const void* k, const void* v, const long long* k_strides, cons
     return d == 64 ? launch_append8<false, 64>(a, narrow, s) : launch_append8<false, 128>(a, narrow, s);
 }
 
+// How a call's rows become items, and its workspace: meta (T and each item's first unit, int64),
+// the partial L and O (fp32) of slots = CTAs + items, RT rows each.
+struct Dec8Plan {
+    int rt;       // rows of a tile: the smallest of 4, 8, 16 that holds a head's (d = 64: two heads') rows
+    int nch, RC;  // chunks a head's rows are cut into, and rows of a chunk
+    int HV;
+    long long items, ctas;
+    size_t meta, lse, total;
+};
+
+bool dec8_plan(int B, int Hq, int Hkv, int Nq, int d, Dec8Plan& p) {
+    const int sms = fa_host::sm_count();
+    if (sms <= 0) return false;
+    const int R = Hq / Hkv * (Nq > 0 ? Nq : 1), heads = d == 64 ? 2 : 1;
+    p.rt = heads * R <= 4 ? 4 : heads * R <= 8 ? 8 : 16;
+    const int most = p.rt / heads;
+    p.nch = (R + most - 1) / most;
+    p.RC = (R + p.nch - 1) / p.nch;
+    p.HV = (Hkv + heads - 1) / heads * p.nch;
+    p.items = static_cast<long long>(B) * p.HV;
+    p.ctas = static_cast<long long>(sms) * fa::kDec8Ctas;
+    const size_t slots = static_cast<size_t>(p.items + p.ctas) * p.rt;
+    auto round = [](size_t x) { return (x + 255) & ~size_t(255); };
+    p.meta = round((1 + p.items) * sizeof(long long));
+    p.lse = round(slots * sizeof(float));
+    p.total = p.meta + p.lse + round(slots * d * sizeof(float));
+    return true;
+}
+
+// Codes [outer, rows, row bytes]: boxes of `box` rows x 128 bytes.
+fa_status code_map(CUtensorMap* m, const void* base, int64_t row, int64_t rows, int64_t outer, int box) {
+    return fa_host::make_map_box(m, base, static_cast<int>(row), static_cast<int>(rows), outer, 1, false, row,
+                                 row * rows, row * rows * outer, box, 1, false, 1);
+}
+
+template <auto Kern>
+bool kernel_ready(int smem) {
+    static fa::PerDevice<int> done;
+    int n = 0;
+    return done.get(fa_host::current_device(), [smem](int& v) {
+        v = 1;
+        return cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+    }, &n);
+}
+
+template <bool BF16, int D, bool PAGED, int RT>
+fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode8Args& a, int causal,
+                        bool run_split, cudaStream_t s) {
+    if (run_split) {
+        constexpr auto kern = fa::fa_decode8_kernel<BF16, D == 64, PAGED, RT>;
+        constexpr int smem = fa::Dec8Cfg<BF16, D == 64, RT>::kSmemBytes;
+        if (!kernel_ready<kern>(smem)) return FA_ERR_CUDA;
+        kern<<<a.G, fa::kDec8Threads, smem, s>>>(mk, mv, a, causal);
+        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    }
+    // The merge is a programmatic dependent of the split kernel (griddepcontrol.wait in it).
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hq * a.Nq);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = run_split ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT>, a) != cudaSuccess) return FA_ERR_CUDA;
+    return launched();
+}
+
+template <bool BF16, int D, bool PAGED>
+fa_status launch_dec8_r(int rt, const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode8Args& a, int causal,
+                        bool run_split, cudaStream_t s) {
+    if (rt == 4) return launch_dec8_t<BF16, D, PAGED, 4>(mk, mv, a, causal, run_split, s);
+    if (rt == 8) return launch_dec8_t<BF16, D, PAGED, 8>(mk, mv, a, causal, run_split, s);
+    return launch_dec8_t<BF16, D, PAGED, 16>(mk, mv, a, causal, run_split, s);
+}
+
+template <bool BF16>
+fa_status launch_dec8(int rt, int d, bool paged, const CUtensorMap& mk, const CUtensorMap& mv,
+                      const fa::Decode8Args& a, int causal, bool run_split, cudaStream_t s) {
+    if (d == 64) return paged ? launch_dec8_r<BF16, 64, true>(rt, mk, mv, a, causal, run_split, s)
+                              : launch_dec8_r<BF16, 64, false>(rt, mk, mv, a, causal, run_split, s);
+    return paged ? launch_dec8_r<BF16, 128, true>(rt, mk, mv, a, causal, run_split, s)
+                 : launch_dec8_r<BF16, 128, false>(rt, mk, mv, a, causal, run_split, s);
+}
+
 fa_status decode8(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale, void* o,
                   float* lse, const int* seqlens, const int* block_table, void* workspace, int B, int Hq, int Hkv,
                   int Nq, int Nk, bool paged, int num_pages, int page_size, int max_pages, int d, float scale,
@@ -125,18 +211,37 @@ fa_status decode8(const void* q, const void* k, const void* v, const float* k_sc
         misaligned(workspace, 16) || misaligned(k_scale, 4) || misaligned(v_scale, 4) || misaligned(seqlens, 4) ||
         misaligned(block_table, 4))
         return FA_ERR_MISALIGNED;
+    fa_status st = FA_OK;
     const int g = Hq / Hkv;
     if (static_cast<long long>(g) * Nq > 128) return FA_ERR_UNSUPPORTED;
     if (Hq > 65535 || B > 65535 || static_cast<long long>(B) * Hq * Nq > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     if (Nq == 0) return FA_OK;
+    Dec8Plan pl;
+    if (!dec8_plan(B, Hq, Hkv, Nq, d, pl)) return FA_ERR_CUDA;
+    const long long tiles = pl.items * ((static_cast<long long>(cap) + 127) / 128);
+    if (pl.items > 0x7fffffffLL || tiles > (1LL << 40)) return FA_ERR_UNSUPPORTED;
     fa::Decode8Args a{};
-    a.q = q;
-    a.k = static_cast<const uint8_t*>(k);
-    a.v = static_cast<const uint8_t*>(v);
+    a.err = fa_host::error_word();
+    if (!a.err) return FA_ERR_CUDA;
+    const int box = !paged ? 128 : page_size % 128 == 0 ? 128 : page_size < 64 ? page_size : 64;
+    CUtensorMap mk{}, mv{};
+    if (cap > 0) {
+        // One row of codes as Hkv d columns: a box takes 128 of them (a head, or two of 64; past
+        // an odd number of small heads it reads zeros).
+        const int64_t row = static_cast<int64_t>(Hkv) * d;
+        const int64_t rows = paged ? page_size : Nk, outer = paged ? num_pages : B;
+        if ((st = code_map(&mk, k, row, rows, outer, box)) != FA_OK ||
+            (st = code_map(&mv, v, row, rows, outer, box)) != FA_OK)
+            return st;
+    }
+    a.q = static_cast<const uint16_t*>(q);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    a.o = o;
+    a.o = static_cast<uint16_t*>(o);
     a.lse = lse;
+    a.meta = static_cast<long long*>(workspace);
+    a.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.meta);
+    a.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.meta + pl.lse);
     a.seqlens = seqlens;
     a.block_table = paged ? block_table : nullptr;
     a.B = B;
@@ -144,21 +249,20 @@ fa_status decode8(const void* q, const void* k, const void* v, const float* k_sc
     a.Hkv = Hkv;
     a.group = g;
     a.Nq = Nq;
+    a.R = g * Nq;
     a.cap = cap;
-    a.unit = paged ? page_size : 128;
-    a.per_seq = paged ? max_pages : (Nk + 127) / 128;
+    a.per_seq = paged ? max_pages : static_cast<int>((Nk + 127LL) / 128);
     a.num_pages = num_pages;
+    a.page_size = paged ? page_size : 128;
+    a.page_box = box;
+    a.HV = pl.HV;
+    a.nch = pl.nch;
+    a.RC = pl.RC;
+    a.G = static_cast<int>(tiles < pl.ctas ? (tiles > 0 ? tiles : 1) : pl.ctas);
     a.scale_log2 = scale * kLog2e;
-    const unsigned grid = static_cast<unsigned>(B * Hq * Nq);
     const cudaStream_t s = cu(stream);
-    if (dtype == FA_BF16) {
-        if (d == 64) fa::fa_decode8_rows_kernel<64, true><<<grid, 128, 0, s>>>(a, causal);
-        else fa::fa_decode8_rows_kernel<128, true><<<grid, 128, 0, s>>>(a, causal);
-    } else {
-        if (d == 64) fa::fa_decode8_rows_kernel<64, false><<<grid, 128, 0, s>>>(a, causal);
-        else fa::fa_decode8_rows_kernel<128, false><<<grid, 128, 0, s>>>(a, causal);
-    }
-    return launched();
+    if (dtype == FA_BF16) return launch_dec8<true>(pl.rt, d, paged, mk, mv, a, causal, tiles > 0, s);
+    return launch_dec8<false>(pl.rt, d, paged, mk, mv, a, causal, tiles > 0, s);
 }
 
 }  // namespace
@@ -259,7 +363,9 @@ fa_status fa_cache_append_paged_fp8(const void* k, const void* v, const long lon
 
 size_t fa_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 0 || (d != 64 && d != 128)) return 0;
-    return static_cast<long long>(Hq / Hkv) * Nq > 128 ? 0 : 256;
+    if (static_cast<long long>(Hq / Hkv) * Nq > 128) return 0;
+    Dec8Plan p;
+    return dec8_plan(B, Hq, Hkv, Nq, d, p) ? p.total : 0;
 }
 
 fa_status fa_decode_fp8(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale,
