@@ -48,7 +48,7 @@ struct Decode8Args {
     float* lse;              // [B, Hq, Nq]
     float* o_part;           // [slots, RT, d] normalised partial outputs
     float* lse_part;         // [slots, RT], log2
-    long long* meta;         // [0] = T, [1 + item] = the item's first unit (lengths given)
+    int2* meta;              // [items]: the CTAs that hold an item's first and last tile
     const int* seqlens;      // [B] or null (every sequence has cap keys)
     const int* block_table;  // [B, per_seq]; null: contiguous
     int B, Hq, Hkv, group, Nq, R;
@@ -72,16 +72,16 @@ struct Dec8Cfg {
     static constexpr int NH = (NT * RH + 15) / 16 * 16;           // rows of Q of one KV head
     static constexpr int NQ = PAIR ? 2 * NH : NH;
     static constexpr int kTile = 128 * 128;                       // one K or V tile
-    static constexpr int kUnits = N > 32 ? 5 : 6;                 // ring of tiles: K, V, K, V, ...
-    static constexpr int kQB = N > 16 ? 1 : 2;                    // query buffers
+    static constexpr int kUnits = 5;                              // ring of tiles: K, V, K, V, ...
+    static constexpr int kQB = 2;                                 // query buffers
     static constexpr int kScSlots = 4;                            // tiles of block factors
     static constexpr int kQOff = 0;
     static constexpr int kPOff = kQOff + kQB * NQ * 128;
     static constexpr int kRingOff = kPOff + 2 * N * 128;
     static constexpr int kBarOff = kRingOff + kUnits * kTile;
     static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 6 + 5;
-    static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 112 bytes: dec8_locate
-    static constexpr int kScOff = (kMiscOff + 112 + 15) / 16 * 16;  // float [slots][40]
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 160 bytes: dec8_locate
+    static constexpr int kScOff = (kMiscOff + 160 + 15) / 16 * 16;  // float [slots][40]
     static constexpr int kQfOff = kScOff + kScSlots * 40 * 4;     // float [2][RT]: scale of a query row
     static constexpr int kRedOff = kQfOff + 2 * RT * 4;           // float [2][4][RT]: warps' maxima
     static constexpr int kRowOff = kRedOff + 8 * RT * 4;          // float [4][5][RT]: a warp's row values
@@ -126,7 +126,15 @@ __device__ __forceinline__ Dec8Item dec8_next(const Decode8Args& a, const Dec8It
     return e;
 }
 
-__device__ __forceinline__ long long dec8_split(int c, long long T, int G) { return (static_cast<long long>(c) * T) / G; }
+// a b / c and a / b, in 32 bits where the operands allow it (64-bit divisions are calls).
+__device__ __forceinline__ long long dec8_muldiv(int a, long long b, int c) {
+    if (b < (1 << 20) && a <= 2048) return static_cast<uint32_t>(a) * static_cast<uint32_t>(b) / static_cast<uint32_t>(c);
+    return a * b / c;
+}
+__device__ __forceinline__ int dec8_div(long long a, long long b) {
+    if (a < (1LL << 31) && b < (1LL << 31)) return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+    return static_cast<int>(a / b);
+}
 
 struct Dec8Range {
     long long T, lo, hi;
@@ -144,83 +152,88 @@ __device__ __forceinline__ bool dec8_segment(const Dec8Range& rg, const Dec8Item
 }
 
 // The CTA's range of the T units and the item that holds its first one; called by every
-// thread (it synchronises the CTA). False, for every thread, when the CTA has none.
+// thread (it synchronises the CTA). False, for every thread, when the CTA has none: only
+// min(G, T) CTAs share the units, so each of those has one at least. Uses misc + 8 .. 159.
 __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc, Dec8Range& rg) {
     const int cta = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
     const int warp = warp_id(), lane = lane_id();
     constexpr int kWarps = kDec8Threads / 32;
+    auto range = [&] {
+        const int G = static_cast<int>(min(static_cast<long long>(a.G), rg.T));
+        if (cta >= G) return false;
+        rg.lo = dec8_muldiv(cta, rg.T, G);
+        rg.hi = dec8_muldiv(cta + 1, rg.T, G);
+        return true;
+    };
     int b0;
     long long P0;
     if (a.seqlens) {
         int* found = reinterpret_cast<int*>(misc + 8);
-        int* sh_b0 = reinterpret_cast<int*>(misc + 24);
-        long long* sh_P0 = reinterpret_cast<long long*>(misc + 32);
-        long long* ws = reinterpret_cast<long long*>(misc + 40);  // [8] per-warp sums
+        int* sh_b0 = reinterpret_cast<int*>(misc + 12);
+        long long* sh_P0 = reinterpret_cast<long long*>(misc + 16);
+        long long* ws = reinterpret_cast<long long*>(misc + 32);  // [8] sums of the scanned requests
+        long long* wr = ws + kWarps;                              // [8] sums of the rest
         auto units_of = [&](int b) -> long long {
             if (b >= a.B) return 0;
             const int ntk = (dec8_len(a, b) + 127) / 128;
             return ntk > 0 ? static_cast<long long>(a.HV) * (ntk + kDec8ItemCost) : 0;
         };
-        long long v = 0;
-        for (int b = tid; b < a.B; b += kDec8Threads) v += units_of(b);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (lane == 0) ws[warp] = v;
+        // The first 256 sequences are scanned while the others are only summed; a CTA whose
+        // range starts further on scans on from there.
+        long long x = units_of(tid), rest = 0;
+        for (int b = tid + kDec8Threads; b < a.B; b += kDec8Threads) rest += units_of(b);
+        long long incl = x, run = 0;
         if (tid == 0) *found = 0;
-        __syncthreads();
-        rg.T = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) rg.T += ws[w];
-        if (cta == 0 && tid == 0) a.meta[0] = rg.T;
-        rg.lo = dec8_split(cta, rg.T, a.G);
-        rg.hi = dec8_split(cta + 1, rg.T, a.G);
-        if (rg.lo >= rg.hi) return false;
-        __syncthreads();  // every thread has read ws
-        long long run = 0;
-        for (int base = 0; base < a.B; base += kDec8Threads) {
-            const int b = base + tid;
-            const long long x = units_of(b);
-            long long incl = x;
+        for (int base = 0;; base += kDec8Threads) {
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const long long y = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += y;
             }
             if (lane == 31) ws[warp] = incl;
+            if (base == 0) {
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+                if (lane == 0) wr[warp] = rest;
+            }
             __syncthreads();
-            long long before = 0, total = 0;
+            long long before = 0, total = 0, others = 0;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const long long y = ws[w];
                 if (w < warp) before += y;
                 total += y;
+                others += wr[w];
+            }
+            if (base == 0) {
+                rg.T = total + others;
+                if (!range()) return false;
             }
             const long long excl = run + before + incl - x;
             if (x > 0 && excl <= rg.lo && rg.lo < excl + x) {  // one thread at most
-                *sh_b0 = b;
+                *sh_b0 = base + tid;
                 *sh_P0 = excl;
                 *found = 1;
             }
             __syncthreads();
             if (*found) break;
             run += total;
+            if (base + kDec8Threads >= a.B) return false;  // cannot happen: lo < T
+            x = incl = units_of(base + kDec8Threads + tid);
         }
-        if (!*found) return false;  // cannot happen: lo < T
         b0 = *sh_b0;
         P0 = *sh_P0;
     } else {
         const int ntk = (a.cap + 127) / 128;
         const long long per_b = ntk > 0 ? static_cast<long long>(a.HV) * (ntk + kDec8ItemCost) : 0;
         rg.T = per_b * a.B;
-        rg.lo = dec8_split(cta, rg.T, a.G);
-        rg.hi = dec8_split(cta + 1, rg.T, a.G);
-        if (rg.lo >= rg.hi) return false;
-        b0 = static_cast<int>(rg.lo / per_b);
+        if (!range()) return false;
+        b0 = dec8_div(rg.lo, per_b);
         P0 = b0 * per_b;
     }
     const int len = dec8_len(a, b0);
     const int cost = (len + 127) / 128 + kDec8ItemCost;
-    const int vh = static_cast<int>((rg.lo - P0) / cost);
+    const int vh = dec8_div(rg.lo - P0, cost);
     rg.first = dec8_item(a, b0, vh, len, P0 + static_cast<long long>(vh) * cost);
     return true;
 }
@@ -310,9 +323,12 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
     uint8_t* misc = smem + C::kMiscOff;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
     int* abort_flag = reinterpret_cast<int*>(misc + 4);
-    Dec8Range rg;
-    if (!dec8_locate(args, misc, rg)) return;
-
+    // TMEM first: the SM starts its second CTA only after the first gave up the permit to
+    // allocate (measured: 0.35 us after it, wherever in the kernel that is).
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, C::kTmemCols);
+        tmem_relinquish();
+    }
     uint8_t* sQ = smem + C::kQOff;
     uint8_t* sP = smem + C::kPOff;
     uint8_t* ring = smem + C::kRingOff;
@@ -366,13 +382,15 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_holder, C::kTmemCols);
-        tmem_relinquish();
-    }
+    Dec8Range rg;
+    const bool work = dec8_locate(args, misc, rg);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (!work) {
+        if (warp == 1) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(tmem_holder), C::kTmemCols);
+        return;
+    }
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
     const WaitCtx wc{abort_flag, args.err};
 
@@ -385,10 +403,13 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
         int u = 0;
         bool ok = true;
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
-            if (lane == 0 && args.seqlens && it.cost > 0 && it.P >= rg.lo)  // the item starts in this CTA's range
-                args.meta[1 + static_cast<size_t>(it.b) * args.HV + it.vh] = it.P;
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
+            if (lane == 0) {
+                int2* m = args.meta + static_cast<size_t>(it.b) * args.HV + it.vh;
+                if (j0 == 0) m->x = cta;
+                if (j0 + n == it.ntk) m->y = cta;
+            }
             const int x0 = (it.vh / args.nch) * 128;  // the head's (or pair's) first byte of a row
             const int* bt = PAGED ? args.block_table + static_cast<size_t>(it.b) * args.per_seq : nullptr;
             auto page_of = [&](int kt) {
@@ -538,47 +559,52 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
             const int hh = it.vh / args.nch, ch = it.vh % args.nch;
-            const int cols = PAIR ? lane >> 4 : 0;  // the head whose 64 values this lane's columns hold
-            uint2 raw[RT];
+            // CPR lanes hold a row, 8 values each; RPI rows at a time.
+            constexpr int CPR = D / 8, RPI = 32 / CPR, NI = RT / RPI;
+            const int c = lane % CPR;
+            uint4 raw[NI];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const int hd = PAIR ? r / RH : 0;
-                const int gr = ch * args.RC + (PAIR ? r % RH : r);
+            for (int i = 0; i < NI; ++i) {
+                const int r = i * RPI + lane / CPR;
+                const int hd = PAIR ? r / RH : 0, rr = PAIR ? r % RH : r;
+                const int gr = ch * args.RC + rr;
                 const int head = PAIR ? 2 * hh + hd : hh;
-                raw[r] = make_uint2(0, 0);
-                if (gr < args.R && (PAIR ? r % RH : r) < args.RC && head < args.Hkv && cols == hd) {
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (rr < args.RC && gr < args.R && head < args.Hkv) {
                     const size_t row = (static_cast<size_t>(it.b) * args.Nq + gr / args.group) * args.Hq +
                                        static_cast<size_t>(head) * args.group + gr % args.group;
-                    raw[r] = *reinterpret_cast<const uint2*>(args.q + row * D + (PAIR ? (lane & 15) : lane) * 4);
+                    raw[i] = *reinterpret_cast<const uint4*>(args.q + row * D + c * 8);
                 }
             }
             const int qb = nq % QB;
             if (!(ok = warp_all(mbar_wait(&q_empty[qb], ((nq / QB) & 1) ^ 1u, wc, 127)))) break;
             uint8_t* dst = sQ + qb * C::NQ * 128;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int i = 0; i < NI; ++i) {
+                const int r = i * RPI + lane / CPR;
                 const int hd = PAIR ? r / RH : 0, rr = PAIR ? r % RH : r;
-                float v[4] = {unpack_lo<BF16>(raw[r].x), unpack_hi<BF16>(raw[r].x), unpack_lo<BF16>(raw[r].y),
-                              unpack_hi<BF16>(raw[r].y)};
+                float v[8];
+                unpack8<BF16>(raw[i], v);
                 float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f);
-                const int e = e4m3_exponent(warp_max(top));
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
+#pragma unroll
+                for (int off = CPR / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const int e = e4m3_exponent(top);
                 const float inv = exp2_int(-e);
+                uint32_t t4[4][NT];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] * inv : __uint_as_float(0x7fffffffu);
-                uint32_t c0[NT], c1[NT];
-                e4m3_terms<NT>(pack2<false>(v[0], v[1]), c0);
-                e4m3_terms<NT>(pack2<false>(v[2], v[3]), c1);
-                if (!PAIR || cols == hd) {
+                for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < INFINITY ? v[k] * inv : __uint_as_float(0x7fffffffu);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const int row = hd * C::NH + t * RH + rr;
-                        *reinterpret_cast<uint32_t*>(dst + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) =
-                            c0[t] | (c1[t] << 16);
-                    }
+                for (int k = 0; k < 4; ++k) e4m3_terms<NT>(pack2<false>(v[2 * k], v[2 * k + 1]), t4[k]);
+                const int col = hd * 64 + c * 8;  // this lane's first byte of the row
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int row = hd * C::NH + t * RH + rr;
+                    *reinterpret_cast<uint2*>(dst + row * 128 + (((col >> 4) ^ (row & 7)) << 4) + (col & 15)) =
+                        make_uint2(t4[0][t] | (t4[1][t] << 16), t4[2][t] | (t4[3][t] << 16));
                 }
-                if (lane == 0) qf[(nq & 1) * RT + r] = args.scale_log2 * exp2_int(e);
+                if (c == 0) qf[(nq & 1) * RT + r] = args.scale_log2 * exp2_int(e);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -820,86 +846,77 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
     }
 }
 
-// Merge of the segments of each output row: one block of four warps per row of
-// [B, Nq, Hq] (warp w takes every fourth segment, a lane four values).
-template <int D, bool BF16, int RT>
-__global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+// Merge of the segments of each output row of [B, Nq, Hq]. WIDE: one block of four warps
+// per row (warp w takes every fourth segment), for items split over many CTAs; else one
+// warp per row. A lane holds four values.
+template <int D, bool BF16, int RT, bool WIDE>
+__global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, const int rows) {
     constexpr bool PAIR = D == 64;
     constexpr int RH = PAIR ? RT / 2 : RT;
-    __shared__ float4 part[4][D / 4];
-    const int lane = lane_id(), warp = warp_id();
-    const int h = static_cast<int>(blockIdx.x % a.Hq);
-    const int t = static_cast<int>(blockIdx.x / a.Hq % a.Nq), b = static_cast<int>(blockIdx.x / a.Hq / a.Nq);
+    constexpr int W = WIDE ? 4 : 1;
+    __shared__ float4 part[W][D / 4];
+    const int lane = lane_id(), warp = WIDE ? warp_id() : 0;
+    const int row = WIDE ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * 4 + warp_id();
+    if (row >= rows) return;
+    const int h = row % a.Hq, bt = row / a.Hq;
+    const int t = bt % a.Nq, b = bt / a.Nq;
     const int hk = h / a.group, gr = t * a.group + h % a.group;
     const int vh = (PAIR ? hk / 2 : hk) * a.nch + gr / a.RC;
     const int r = (PAIR ? hk % 2 * RH : 0) + gr % a.RC;
     const size_t item = static_cast<size_t>(b) * a.HV + vh;
+    // Launched as a programmatic dependent of the split kernel: what that wrote may be read
+    // from here on.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 cc = a.meta[item];  // of an item without keys: anything
     const int len = dec8_len(a, b);
-    const int ntk = (len + 127) / 128;
-    long long T = 0, P = 0;
-    if (ntk > 0) {
-        if (a.seqlens) {
-            T = a.meta[0];
-            P = a.meta[1 + item];
-        } else {
-            T = static_cast<long long>(a.B) * a.HV * (ntk + kDec8ItemCost);
-            P = static_cast<long long>(item) * (ntk + kDec8ItemCost);
-        }
-    }
-    // The CTAs whose range holds one of the item's tiles: the largest c with
-    // floor(c T / G) <= t, for its first and its last tile.
-    int c0 = 0, c1 = -1;
-    if (ntk > 0 && T > 0) {
-        c0 = static_cast<int>(((P + kDec8ItemCost + 1) * a.G - 1) / T);
-        c1 = static_cast<int>(((P + kDec8ItemCost + ntk) * a.G - 1) / T);
-    }
-    const bool all_have = T >= a.G;
-    auto has = [&](int c) { return all_have || dec8_split(c, T, a.G) < dec8_split(c + 1, T, a.G); };
-    auto at = [&](int c) { return (static_cast<size_t>(c) + item) * RT + r; };
+    const int c0 = cc.x, c1 = len > 0 ? cc.y : cc.x - 1;
+    const float* lp = a.lse_part + item * RT + r;  // segment of CTA c: lp[c * RT]
+    const float4* op = reinterpret_cast<const float4*>(a.o_part + (item * RT + r) * D) + lane;
     float Lm = -INFINITY;
     bool nan = false;
-    for (int c = c0 + lane; c <= c1; c += 32)
-        if (has(c)) {
-            const float L = a.lse_part[at(c)];
-            Lm = fmaxf(Lm, L);
-            nan |= L != L;
-        }
+    for (int c = c0 + lane; c <= c1; c += 32) {
+        const float L = lp[static_cast<size_t>(c) * RT];
+        Lm = fmaxf(Lm, L);
+        nan |= L != L;
+    }
     Lm = warp_max(Lm);
     nan = __any_sync(0xffffffffu, nan);
     const float ref = Lm == -INFINITY ? 0.f : Lm;
     float wsum = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32)
-        if (has(c)) wsum += ex2_approx(a.lse_part[at(c)] - ref);
+    for (int c = c0 + lane; c <= c1; c += 32) wsum += ex2_approx(lp[static_cast<size_t>(c) * RT] - ref);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (lane < D / 4) {
-#pragma unroll 2
-        for (int c = c0 + warp; c <= c1; c += 4) {
-            if (!has(c)) continue;
-            const float w = ex2_approx(a.lse_part[at(c)] - ref);
-            const float4 x = reinterpret_cast<const float4*>(a.o_part + at(c) * D)[lane];
+#pragma unroll 4
+        for (int c = c0 + warp; c <= c1; c += W) {
+            const float w = ex2_approx(lp[static_cast<size_t>(c) * RT] - ref);
+            const float4 x = op[static_cast<size_t>(c) * (RT * D / 4)];
             acc.x = fmaf(w, x.x, acc.x);
             acc.y = fmaf(w, x.y, acc.y);
             acc.z = fmaf(w, x.z, acc.z);
             acc.w = fmaf(w, x.w, acc.w);
         }
-        part[warp][lane] = acc;
+        if (WIDE) part[warp][lane] = acc;
     }
-    __syncthreads();
-    if (warp != 0 || lane >= D / 4) return;
+    if constexpr (WIDE) {
+        __syncthreads();
+        if (warp != 0) return;
+        if (lane < D / 4) {
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
-        const float4 y = part[w][lane];
-        acc.x += y.x;
-        acc.y += y.y;
-        acc.z += y.z;
-        acc.w += y.w;
+            for (int w = 1; w < W; ++w) {
+                const float4 y = part[w][lane];
+                acc.x += y.x;
+                acc.y += y.y;
+                acc.z += y.z;
+                acc.w += y.w;
+            }
+        }
     }
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    uint16_t* o = a.o + static_cast<size_t>(blockIdx.x) * D + lane * 4;
-    *reinterpret_cast<uint2*>(o) = make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+    if (lane < D / 4)
+        *reinterpret_cast<uint2*>(a.o + static_cast<size_t>(row) * D + lane * 4) =
+            make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
     if (lane == 0)
         a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Nq + t] =
             nan ? __uint_as_float(0x7fffffffu) : (wsum == 0.f ? -INFINITY : (Lm + log2f(wsum)) * kLn2);

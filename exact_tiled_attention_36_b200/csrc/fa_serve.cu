@@ -104,8 +104,8 @@ fa_status append8(const void* k, const void* v, const long long* k_strides, cons
     return d == 64 ? launch_append8<false, 64>(a, narrow, s) : launch_append8<false, 128>(a, narrow, s);
 }
 
-// How a call's rows become items, and its workspace: meta (T and each item's first unit, int64),
-// the partial L and O (fp32) of slots = CTAs + items, RT rows each.
+// How a call's rows become items, and its workspace: meta (each item's first and last CTA), the
+// partial L and O (fp32) of slots = CTAs + items, RT rows each.
 struct Dec8Plan {
     int rt;       // rows of a tile: the smallest of 4, 8, 16 that holds a head's (d = 64: two heads') rows
     int nch, RC;  // chunks a head's rows are cut into, and rows of a chunk
@@ -127,7 +127,7 @@ bool dec8_plan(int B, int Hq, int Hkv, int Nq, int d, Dec8Plan& p) {
     p.ctas = static_cast<long long>(sms) * fa::kDec8Ctas;
     const size_t slots = static_cast<size_t>(p.items + p.ctas) * p.rt;
     auto round = [](size_t x) { return (x + 255) & ~size_t(255); };
-    p.meta = round((1 + p.items) * sizeof(long long));
+    p.meta = round(p.items * sizeof(int2));
     p.lse = round(slots * sizeof(float));
     p.total = p.meta + p.lse + round(slots * d * sizeof(float));
     return true;
@@ -161,7 +161,10 @@ fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::
     }
     // The merge is a programmatic dependent of the split kernel (griddepcontrol.wait in it).
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hq * a.Nq);
+    // A row's segments: about CTAs / items, one or two more where ranges cross.
+    const int rows = a.B * a.Hq * a.Nq;
+    const bool wide = a.G > 6LL * a.B * a.HV;
+    cfg.gridDim = dim3(wide ? rows : (rows + 3) / 4);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -169,7 +172,9 @@ fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = run_split ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT>, a) != cudaSuccess) return FA_ERR_CUDA;
+    if ((wide ? cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT, true>, a, rows)
+              : cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT, false>, a, rows)) != cudaSuccess)
+        return FA_ERR_CUDA;
     return launched();
 }
 
@@ -239,7 +244,7 @@ fa_status decode8(const void* q, const void* k, const void* v, const float* k_sc
     a.v_scale = v_scale;
     a.o = static_cast<uint16_t*>(o);
     a.lse = lse;
-    a.meta = static_cast<long long*>(workspace);
+    a.meta = static_cast<int2*>(workspace);
     a.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.meta);
     a.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.meta + pl.lse);
     a.seqlens = seqlens;
