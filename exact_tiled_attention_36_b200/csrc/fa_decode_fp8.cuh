@@ -29,10 +29,12 @@
 // an item takes two adjacent KV heads, whose code rows form one 128-byte row; S^T of each
 // is a product over its own 64 bytes, O^T lanes 64 k .. hold head k.
 //
-// Two CTAs share an SM (each 3 key tiles deep), so one's softmax overlaps the other's
-// products and loads. Warp roles (256 threads): warp 0 TMA producer (its lanes issue the
-// boxes of a tile), warp 1 TMEM and the MMA thread, warp 2 block factors, warp 3 the
-// queries' terms, warps 4-7 softmax (thread l: key l of every tile, then d index l of O).
+// Two CTAs share an SM, so one's softmax overlaps the other's products and loads. Warp
+// roles: warp 0 TMA producer (its lanes issue the boxes of a tile), warp 1 TMEM and the
+// MMA thread, warp 2 block factors, warp 3 the queries' terms, then NW softmax warpgroups,
+// each with RT / NW of the rows (thread l: key l of every tile, then d index l of O).
+// With all 16 rows in one warpgroup the loop was bound by instruction fetch (2.2 warps
+// waiting for instructions per issue) and by its own latency; two halve its length.
 #pragma once
 
 #include "fa_cache.cuh"
@@ -60,12 +62,14 @@ struct Decode8Args {
     int* err;
 };
 
-constexpr int kDec8Threads = 256;
 constexpr int kDec8Ctas = 2;       // per SM
 constexpr int kDec8ItemCost = 2;   // units of a segment's fixed work (see kDecItemCost)
 
 template <bool BF16, bool PAIR, int RT>
 struct Dec8Cfg {
+    static constexpr int NW = RT == 4 ? 1 : 2;                    // softmax warpgroups
+    static constexpr int RW = RT / NW;                            // rows of one
+    static constexpr int kThreads = 128 + 128 * NW;
     static constexpr int NT = BF16 ? 2 : 3;                       // terms of a query and of a weight
     static constexpr int N = (NT * RT + 15) / 16 * 16;            // rows of P
     static constexpr int RH = PAIR ? RT / 2 : RT;                 // rows of one KV head
@@ -79,13 +83,14 @@ struct Dec8Cfg {
     static constexpr int kPOff = kQOff + kQB * NQ * 128;
     static constexpr int kRingOff = kPOff + 2 * N * 128;
     static constexpr int kBarOff = kRingOff + kUnits * kTile;
-    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 6 + 5;
-    static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 160 bytes: dec8_locate
-    static constexpr int kScOff = (kMiscOff + 160 + 15) / 16 * 16;  // float [slots][40]
+    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 8 + 3 * NW;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 224 bytes: dec8_locate
+    static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][40]
     static constexpr int kQfOff = kScOff + kScSlots * 40 * 4;     // float [2][RT]: scale of a query row
-    static constexpr int kRedOff = kQfOff + 2 * RT * 4;           // float [2][4][RT]: warps' maxima
-    static constexpr int kRowOff = kRedOff + 8 * RT * 4;          // float [4][5][RT]: a warp's row values
-    static constexpr int kSumOff = kRowOff + 20 * RT * 4;         // float [4][RT]: warps' sums
+    // A warpgroup's share of each: its RW rows.
+    static constexpr int kRedOff = kQfOff + 2 * RT * 4;           // float [NW][2][4][RW]: warps' maxima
+    static constexpr int kRowOff = kRedOff + 8 * RT * 4;          // float [NW][4][5][RW]: a warp's row values
+    static constexpr int kSumOff = kRowOff + 20 * RT * 4;         // float [NW][4][RW]: warps' sums
     static constexpr int kSmemBytes = kSumOff + 4 * RT * 4;
     static constexpr uint32_t kColO = 2 * NQ;                     // S^T buffers at 0 and NQ
     static constexpr uint32_t kCols = 2 * NQ + 2 * N;
@@ -153,11 +158,12 @@ __device__ __forceinline__ bool dec8_segment(const Dec8Range& rg, const Dec8Item
 
 // The CTA's range of the T units and the item that holds its first one; called by every
 // thread (it synchronises the CTA). False, for every thread, when the CTA has none: only
-// min(G, T) CTAs share the units, so each of those has one at least. Uses misc + 8 .. 159.
+// min(G, T) CTAs share the units, so each of those has one at least. Uses misc + 8 .. 223.
+template <int THREADS>
 __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc, Dec8Range& rg) {
     const int cta = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
     const int warp = warp_id(), lane = lane_id();
-    constexpr int kWarps = kDec8Threads / 32;
+    constexpr int kWarps = THREADS / 32;
     auto range = [&] {
         const int G = static_cast<int>(min(static_cast<long long>(a.G), rg.T));
         if (cta >= G) return false;
@@ -171,20 +177,20 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
         int* found = reinterpret_cast<int*>(misc + 8);
         int* sh_b0 = reinterpret_cast<int*>(misc + 12);
         long long* sh_P0 = reinterpret_cast<long long*>(misc + 16);
-        long long* ws = reinterpret_cast<long long*>(misc + 32);  // [8] sums of the scanned requests
-        long long* wr = ws + kWarps;                              // [8] sums of the rest
+        long long* ws = reinterpret_cast<long long*>(misc + 32);  // sums of the scanned sequences
+        long long* wr = ws + kWarps;                              // sums of the rest
         auto units_of = [&](int b) -> long long {
             if (b >= a.B) return 0;
             const int ntk = (dec8_len(a, b) + 127) / 128;
             return ntk > 0 ? static_cast<long long>(a.HV) * (ntk + kDec8ItemCost) : 0;
         };
-        // The first 256 sequences are scanned while the others are only summed; a CTA whose
+        // The first THREADS sequences are scanned while the others are only summed; a CTA whose
         // range starts further on scans on from there.
         long long x = units_of(tid), rest = 0;
-        for (int b = tid + kDec8Threads; b < a.B; b += kDec8Threads) rest += units_of(b);
+        for (int b = tid + THREADS; b < a.B; b += THREADS) rest += units_of(b);
         long long incl = x, run = 0;
         if (tid == 0) *found = 0;
-        for (int base = 0;; base += kDec8Threads) {
+        for (int base = 0;; base += THREADS) {
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const long long y = __shfl_up_sync(0xffffffffu, incl, off);
@@ -218,8 +224,8 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
             __syncthreads();
             if (*found) break;
             run += total;
-            if (base + kDec8Threads >= a.B) return false;  // cannot happen: lo < T
-            x = incl = units_of(base + kDec8Threads + tid);
+            if (base + THREADS >= a.B) return false;  // cannot happen: lo < T
+            x = incl = units_of(base + THREADS + tid);
         }
         b0 = *sh_b0;
         P0 = *sh_P0;
@@ -309,11 +315,12 @@ __device__ __forceinline__ void e4m3_terms(uint32_t x, uint32_t (&c)[NT]) {
 
 // ------------------------------------------------------------------- split kernel
 template <bool BF16, bool PAIR, bool PAGED, int RT>
-__global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
+__global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     fa_decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const Decode8Args args, const int causal) {
     using C = Dec8Cfg<BF16, PAIR, RT>;
     constexpr int NT = C::NT, U = C::kUnits, QB = C::kQB, SC = C::kScSlots, RH = C::RH;
+    constexpr int NW = C::NW, RW = C::RW, THREADS = C::kThreads;
     constexpr int D = PAIR ? 64 : 128;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (!smem_base_ok(smem, args.err)) return;
@@ -343,14 +350,13 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
     uint64_t* pv_done = p_full + 2;    // [2] O_t of the tile complete
     uint64_t* mma_done = pv_done + 2;
     uint64_t* sm_done = mma_done + 1;
-    uint64_t* meet_bar = sm_done + 1;  // [2] softmax warps, per tile parity
-    uint64_t* sum_bar = meet_bar + 2;  // once per segment
+    uint64_t* meet_bar = sm_done + 1;  // [NW][3]: a warpgroup's warps, per tile parity and per segment
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
 
     // Rows of P past the terms are zeros (those of Q are never looked at: their columns
     // of S^T are not read, but they must hold codes that are there).
-    for (int i = tid; i < (C::kRingOff - C::kQOff) / 16; i += kDec8Threads)
+    for (int i = tid; i < (C::kRingOff - C::kQOff) / 16; i += THREADS)
         reinterpret_cast<uint4*>(smem + C::kQOff)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (tid == 0) {
@@ -360,21 +366,20 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
         }
         for (int i = 0; i < QB; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 5);  // the last S^T product, and each softmax warp's last use of the scales
+            mbar_init(&q_empty[i], 1 + 4 * NW);  // the last S^T product, and each softmax warp's last use of the scales
         }
         for (int i = 0; i < SC; ++i) {
             mbar_init(&sc_full[i], 1);
-            mbar_init(&sc_empty[i], 4);
+            mbar_init(&sc_empty[i], 4 * NW);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&p_full[i], 128 * NW);
             mbar_init(&pv_done[i], 1);
-            mbar_init(&meet_bar[i], 4);
         }
-        mbar_init(sum_bar, 4);
+        for (int i = 0; i < 3 * NW; ++i) mbar_init(&meet_bar[i], 4);
         mbar_init(mma_done, 1);
-        mbar_init(sm_done, 128);
+        mbar_init(sm_done, 128 * NW);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
         tma_prefetch_desc(&tm_v);
     }
     Dec8Range rg;
-    const bool work = dec8_locate(args, misc, rg);
+    const bool work = dec8_locate<THREADS>(args, misc, rg);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -613,18 +618,23 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
         }
     } else {
         // ------------------------------------------------------------ softmax, output
-        const int w4 = warp - 4;
+        const int wg = (warp - 4) >> 2, w4 = warp & 3;  // warp % 4 is the TMEM lane quarter it reaches
+        constexpr bool kMixed = PAIR && RW > RH;         // one warpgroup holds both heads' rows
+        const int first = wg * RW;                       // its first row of the tile
+        const int wg_hd = PAIR && !kMixed ? first / RH : 0;
         const int l_idx = w4 * 32 + lane;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
-        float* red = reinterpret_cast<float*>(smem + C::kRedOff);  // [2][4][RT]
-        float* row_m = reinterpret_cast<float*>(smem + C::kRowOff) + w4 * 5 * RT;  // this warp's copies of row values
-        float* row_f = row_m + RT;      // [2]: 2^(m_tile - m_run), times the tile's V factor from the second use on
-        float* row_a = row_f + 2 * RT;  // 2^(m_run before - m_run)
-        int* row_hi = reinterpret_cast<int*>(row_a + RT);  // keys a row sees
+        float* red = reinterpret_cast<float*>(smem + C::kRedOff) + wg * 8 * RW;  // [2][4][RW]
+        float* row_m = reinterpret_cast<float*>(smem + C::kRowOff) + (wg * 4 + w4) * 5 * RW;  // this warp's row values
+        float* row_f = row_m + RW;      // [2]: 2^(m_tile - m_run), times the tile's V factor from the second use on
+        float* row_a = row_f + 2 * RW;  // 2^(m_run before - m_run)
+        int* row_hi = reinterpret_cast<int*>(row_a + RW);  // keys a row sees
+        uint64_t* meets = meet_bar + 3 * wg;
         const int box = l_idx / args.page_box;
-        // Row `lane` of the tile: its head of the pair, its query token.
-        const int my_hd = PAIR ? lane / RH : 0, my_rr = PAIR ? lane % RH : lane;
-        float* sums = reinterpret_cast<float*>(smem + C::kSumOff);  // [4][RT], once per segment
+        // Row `lane` of the warpgroup: its head of the pair, its place among that head's rows.
+        const int my_r = first + (lane < RW ? lane : 0);
+        const int my_hd = PAIR ? my_r / RH : 0, my_rr = PAIR ? my_r % RH : my_r;
+        float* sums = reinterpret_cast<float*>(smem + C::kSumOff) + wg * 4 * RW;  // [4][RW], once per segment
         int gk = 0, nq = 0;
         bool ok = true;
         auto meet = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
@@ -639,31 +649,31 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
             const int hh = it.vh / args.nch, ch = it.vh % args.nch;
             const int my_gr = ch * args.RC + my_rr;  // this lane's row in its head's group
             __syncwarp();
-            if (lane < RT) row_hi[lane] = causal ? min(it.len, my_gr / args.group + it.len - args.Nq + 1) : it.len;
+            if (lane < RW) row_hi[lane] = causal ? min(it.len, my_gr / args.group + it.len - args.Nq + 1) : it.len;
             __syncwarp();
             const int all_hi = causal ? it.len - args.Nq + 1 : it.len;  // keys below it are seen by every row
             ok = warp_all(mbar_wait(&q_full[nq % QB], (nq / QB) & 1, wc, 128));
             if (!ok) break;
-            const float* my_qf = qf + (nq & 1) * RT;
-            float acc[RT], l[RT];
+            const float* my_qf = qf + (nq & 1) * RT + first;
+            float acc[RW], l[RW];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) acc[r] = l[r] = 0.f;
+            for (int r = 0; r < RW; ++r) acc[r] = l[r] = 0.f;
             float m_run = -INFINITY;  // of row `lane`
             // acc += f O_t of tile gg, whose factors sit in row_f of its parity.
             auto drain = [&](int gg) -> bool {
                 const int b = gg & 1;
                 if (!warp_all(mbar_wait(&pv_done[b], (gg >> 1) & 1, wc, 129))) return false;
                 tc_fence_after();
-                uint32_t o[NT][RT];
+                uint32_t o[NT][RW];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    tmem_ldn<RT>(lane_base + C::kColO + static_cast<uint32_t>(b * C::N + t * RT), o[t]);
+                    tmem_ldn<RW>(lane_base + C::kColO + static_cast<uint32_t>(b * C::N + t * RT + first), o[t]);
                 tmem_ld_done();
 #pragma unroll
-                for (int t = 0; t < NT; ++t) tie<RT>(o[t]);
+                for (int t = 0; t < NT; ++t) tie<RW>(o[t]);
 #pragma unroll
-                for (int r = 0; r < RT; r += 4) {
-                    const float4 f4 = rows4(row_f + b * RT, r);
+                for (int r = 0; r < RW; r += 4) {
+                    const float4 f4 = rows4(row_f + b * RW, r);
                     const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -680,28 +690,29 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                 ok = warp_all(mbar_wait(&sc_full[slot], (gg / SC) & 1, wc, 130));
                 if (!ok) break;
                 const float* s_sc = sc + slot * 40;
-                const float kf0 = s_sc[box], kf1 = PAIR ? s_sc[8 + box] : 0.f;
-                const float vs0 = s_sc[16 + box], vs1 = PAIR ? s_sc[24 + box] : 0.f;
-                const float my_vm = s_sc[32 + (lane < RT ? my_hd : 0)];
+                const float kf0 = s_sc[8 * wg_hd + box], kf1 = kMixed ? s_sc[8 + box] : 0.f;
+                const float vs0 = s_sc[16 + 8 * wg_hd + box], vs1 = kMixed ? s_sc[24 + box] : 0.f;
+                const float my_vm = s_sc[32 + my_hd];
                 ok = warp_all(mbar_wait(&s_full[par], (gg >> 1) & 1, wc, 131));
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc_empty[slot]);
                 tc_fence_after();
-                float x[RT];
+                float x[RW];
                 {
-                    uint32_t s[NT][RT];
-                    const uint32_t s_addr = lane_base + static_cast<uint32_t>(par * C::NQ);
+                    uint32_t s[NT][RW];
+                    const uint32_t s_addr = lane_base + static_cast<uint32_t>(
+                        par * C::NQ + (PAIR ? first / RH * C::NH + first % RH : first));
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        tmem_ldn<RH>(s_addr + t * RH, s[t]);
-                        if constexpr (PAIR) tmem_ldn<RH>(s_addr + C::NH + t * RH, s[t] + RH);
+                        tmem_ldn<kMixed ? RH : RW>(s_addr + t * RH, s[t]);
+                        if constexpr (kMixed) tmem_ldn<RH>(s_addr + C::NH + t * RH, s[t] + RH);
                     }
                     tmem_ld_done();
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) tie<RT>(s[t]);
+                    for (int t = 0; t < NT; ++t) tie<RW>(s[t]);
 #pragma unroll
-                    for (int r = 0; r < RT; r += 4) {
+                    for (int r = 0; r < RW; r += 4) {
                         const float4 f4 = rows4(my_qf, r);
                         const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
@@ -709,7 +720,7 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                             float v = __uint_as_float(s[NT - 1][r + i]);
 #pragma unroll
                             for (int t = NT - 2; t >= 0; --t) v = fmaf(v, 0.0625f, __uint_as_float(s[t][r + i]));
-                            x[r + i] = v * f[i] * (PAIR && r + i >= RH ? kf1 : kf0);
+                            x[r + i] = v * f[i] * (kMixed && r + i >= RH ? kf1 : kf0);
                         }
                     }
                 }
@@ -720,22 +731,22 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                 const int key = (j0 + j) * 128 + l_idx;
                 if ((j0 + j + 1) * 128 > all_hi) {
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
+                    for (int r = 0; r < RW; ++r)
                         if (key >= row_hi[r]) x[r] = -INFINITY;
                 }
                 // Every row's largest score of the tile: over the warp, then the four warps.
-                float* rd = red + par * 4 * RT;
+                float* rd = red + par * 4 * RW;
 #pragma unroll
-                for (int r = 0; r < RT; r += 4) {
+                for (int r = 0; r < RW; r += 4) {
                     const float4 v = make_float4(warp_max(x[r]), warp_max(x[r + 1]), warp_max(x[r + 2]), warp_max(x[r + 3]));
-                    if (lane == 0) *reinterpret_cast<float4*>(rd + w4 * RT + r) = v;
+                    if (lane == 0) *reinterpret_cast<float4*>(rd + w4 * RW + r) = v;
                 }
-                ok = meet(&meet_bar[par], (gg >> 1) & 1, 132);
+                ok = meet(&meets[par], (gg >> 1) & 1, 132);
                 if (!ok) break;
                 // Lane r takes row r's running values.
                 bool moved = false;
-                if (lane < RT) {
-                    const float mt = fmaxf(fmaxf(rd[lane], rd[RT + lane]), fmaxf(rd[2 * RT + lane], rd[3 * RT + lane]));
+                if (lane < RW) {
+                    const float mt = fmaxf(fmaxf(rd[lane], rd[RW + lane]), fmaxf(rd[2 * RW + lane], rd[3 * RW + lane]));
                     float alpha = 1.f;
                     if (mt > m_run + kRescaleThreshold) {
                         alpha = ex2_approx(m_run - mt);  // 0 for the first keys
@@ -745,7 +756,7 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                     const bool none = mt == -INFINITY;
                     const float f = none ? 0.f : ex2_approx(mt - m_run);
                     row_m[lane] = none ? 0.f : -mt;
-                    row_f[par * RT + lane] = f;
+                    row_f[par * RW + lane] = f;
                     row_a[lane] = alpha;
                 }
                 moved = __any_sync(0xffffffffu, moved);
@@ -753,8 +764,8 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                 // P = 2^(x - m_tile), its sum in the running scale, and its terms times V's share.
                 uint8_t* pb = sP + par * C::N * 128;
 #pragma unroll
-                for (int r = 0; r < RT; r += 4) {
-                    const float4 m4 = rows4(row_m, r), f4 = rows4(row_f + par * RT, r);
+                for (int r = 0; r < RW; r += 4) {
+                    const float4 m4 = rows4(row_m, r), f4 = rows4(row_f + par * RW, r);
                     const float mm[4] = {m4.x, m4.y, m4.z, m4.w}, ff[4] = {f4.x, f4.y, f4.z, f4.w};
                     if (moved) {
                         const float4 a4 = rows4(row_a, r);
@@ -769,11 +780,11 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                         l[r + i] = fmaf(p0, ff[i], l[r + i]);
                         l[r + i + 1] = fmaf(p1, ff[i + 1], l[r + i + 1]);
                         uint32_t c[NT];
-                        e4m3_terms<NT>(pack2<false>(p0 * (PAIR && r + i >= RH ? vs1 : vs0),
-                                                    p1 * (PAIR && r + i + 1 >= RH ? vs1 : vs0)), c);
+                        e4m3_terms<NT>(pack2<false>(p0 * (kMixed && r + i >= RH ? vs1 : vs0),
+                                                    p1 * (kMixed && r + i + 1 >= RH ? vs1 : vs0)), c);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            const int n0 = t * RT + r + i;
+                            const int n0 = t * RT + first + r + i;
                             pb[n0 * 128 + (((l_idx >> 4) ^ (n0 & 7)) << 4) + (l_idx & 15)] = static_cast<uint8_t>(c[t]);
                             pb[(n0 + 1) * 128 + (((l_idx >> 4) ^ ((n0 + 1) & 7)) << 4) + (l_idx & 15)] =
                                 static_cast<uint8_t>(c[t] >> 8);
@@ -788,7 +799,7 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                     if (!ok) break;
                     const int v0 = it.len & 127;
                     uint4* vt = reinterpret_cast<uint4*>(ring + (uv % U) * C::kTile + v0 * 128);
-                    for (int i = l_idx; i < (128 - v0) * 8; i += 128) vt[i] = make_uint4(0, 0, 0, 0);
+                    for (int i = wg * 128 + l_idx; i < (128 - v0) * 8; i += 128 * NW) vt[i] = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -797,7 +808,7 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                 if (j > 0 && !(ok = drain(gg - 1))) break;
                 if (moved) {
 #pragma unroll
-                    for (int r = 0; r < RT; r += 4) {
+                    for (int r = 0; r < RW; r += 4) {
                         const float4 a4 = rows4(row_a, r);
                         acc[r] *= a4.x;
                         acc[r + 1] *= a4.y;
@@ -807,7 +818,7 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
                 }
                 // The factor of O_t carries the tile's V factor too.
                 __syncwarp();
-                if (lane < RT) row_f[par * RT + lane] *= my_vm;
+                if (lane < RW) row_f[par * RW + lane] *= my_vm;
                 __syncwarp();
             }
             if (!ok) break;
@@ -816,26 +827,27 @@ __global__ void __launch_bounds__(kDec8Threads, kDec8Ctas)
             // Row sums over the 128 keys' threads (written again a segment later, after
             // every warp has met at a tile in between).
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int r = 0; r < RW; ++r) {
                 float a = l[r];
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-                if (lane == 0) sums[w4 * RT + r] = a;
+                if (lane == 0) sums[w4 * RW + r] = a;
             }
-            if (lane < RT) row_m[lane] = m_run;
-            ok = meet(sum_bar, nq & 1, 134);
+            if (lane < RW) row_m[lane] = m_run;
+            ok = meet(&meets[2], nq & 1, 134);
             if (!ok) break;
             const size_t slot = static_cast<size_t>(cta) + static_cast<size_t>(it.b) * args.HV + it.vh;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const int hd = PAIR ? r / RH : 0, rr = PAIR ? r % RH : r;
+            for (int r = 0; r < RW; ++r) {
+                const int rt = first + r;
+                const int hd = PAIR ? rt / RH : 0, rr = PAIR ? rt % RH : rt;
                 const int head = PAIR ? 2 * hh + hd : hh;
                 if (rr < args.RC && ch * args.RC + rr < args.R && head < args.Hkv) {
-                    const float lt = sums[r] + sums[RT + r] + sums[2 * RT + r] + sums[3 * RT + r];
+                    const float lt = sums[r] + sums[RW + r] + sums[2 * RW + r] + sums[3 * RW + r];
                     // no key: 0; NaN stays NaN
-                    const float v = lt == 0.f ? 0.f : acc[r] / lt;
-                    if (!PAIR || (l_idx >> 6) == hd) args.o_part[(slot * RT + r) * D + (PAIR ? l_idx & 63 : l_idx)] = v;
-                    if (l_idx == r) args.lse_part[slot * RT + r] = lt == 0.f ? -INFINITY : row_m[r] + log2f(lt);
+                    const float v = lt == 0.f ? 0.f : __fdividef(acc[r], lt);
+                    if (!PAIR || (l_idx >> 6) == hd) args.o_part[(slot * RT + rt) * D + (PAIR ? l_idx & 63 : l_idx)] = v;
+                    if (l_idx == r) args.lse_part[slot * RT + rt] = lt == 0.f ? -INFINITY : row_m[r] + log2f(lt);
                 }
             }
             gk += n;

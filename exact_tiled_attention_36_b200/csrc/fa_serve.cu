@@ -154,9 +154,9 @@ fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::
                         bool run_split, cudaStream_t s) {
     if (run_split) {
         constexpr auto kern = fa::fa_decode8_kernel<BF16, D == 64, PAGED, RT>;
-        constexpr int smem = fa::Dec8Cfg<BF16, D == 64, RT>::kSmemBytes;
-        if (!kernel_ready<kern>(smem)) return FA_ERR_CUDA;
-        kern<<<a.G, fa::kDec8Threads, smem, s>>>(mk, mv, a, causal);
+        using C = fa::Dec8Cfg<BF16, D == 64, RT>;
+        if (!kernel_ready<kern>(C::kSmemBytes)) return FA_ERR_CUDA;
+        kern<<<a.G, C::kThreads, C::kSmemBytes, s>>>(mk, mv, a, causal);
         if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     }
     // The merge is a programmatic dependent of the split kernel (griddepcontrol.wait in it).
