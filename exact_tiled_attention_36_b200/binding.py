@@ -520,51 +520,98 @@ def attention_fwd_fp8(q8, k8, v8, q_scale, k_scale, v_scale, scale: float | None
 # Serving. These write caches and tables in place, so nothing is copied or converted on the way:
 # every tensor must already have the type and the (contiguous) layout the entry point takes, and all
 # must lie on one device, which need not be the current one. `stream`: as above, a stream of that device.
-def _on(device, fn):
-    """fn() with `device` current."""
-    import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return fn()
-    with torch.cuda.device(device):
-        return fn()
+# A decode step makes these calls once per layer, next to kernels of a few microseconds, so the
+# checks are one expression per tensor and only a failing one looks for the message.
+_T = None  # torch, imported with the first call
 
 
-def _own(t, name: str, dtypes, device, shape=None):
-    """`t` as it is, or an error: its type, device, layout and (where given) shape."""
+def _torch():
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
+
+
+def _fits(t, dtype, index, shape) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+
+
+def _own(t, name: str, dtypes, index, shape):
+    """`t` as it is, or an error: its type, device, shape and layout."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(x) for x in dtypes)}, got {t.dtype}")
-    if t.device != device or not t.is_cuda:
+    if not t.is_cuda or t.get_device() != index:
         raise ValueError(f"{name} must be on the CUDA device of the other tensors")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
 
 
-def _temporary(make, device, stream):
-    """A buffer of this call alone: kept from other uses until `stream` has run the call."""
-    import torch
-    t = make()
+def _need(t, name, dtype, index, shape):
+    return t if _fits(t, dtype, index, shape) else _own(t, name, (dtype,), index, shape)
+
+
+def _codes(t, name, index, shape):
+    """E4M3 codes: uint8 or float8_e4m3fn."""
+    T = _torch()
+    if _fits(t, T.uint8, index, shape):
+        return t
+    return _own(t, name, (T.uint8, T.float8_e4m3fn), index, shape)
+
+
+def _call(index: int, stream, what: str, fn, *args):
+    """fn(*args, stream handle) with device `index` current; its status as an exception."""
+    T = _torch()
+    if index == T._C._cuda_getDevice():
+        st = fn(*args, T._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+    else:
+        with T.cuda.device(index):
+            st = fn(*args, _stream(stream))
+    if st != FA_OK:
+        raise FAError(st, what)
+
+
+def _temporary(t, stream):
+    """A buffer of this call alone, kept from other uses until `stream` has run the call."""
     if stream is not None:
-        t.record_stream(stream if hasattr(stream, "cuda_stream") else
-                        torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else
-                        torch.cuda.default_stream(device))
+        T = _torch()
+        if not hasattr(stream, "cuda_stream"):
+            stream = T.cuda.ExternalStream(int(stream), device=t.device) if int(stream) else \
+                T.cuda.default_stream(t.device)
+        t.record_stream(stream)
     return t
 
 
-def _rows(t, name: str, device):
+def _rows(t, name: str, index):
     """(token, head) strides of new rows [T, Hkv, d], any 16-byte multiples; None when contiguous."""
-    if t.dim() != 3 or t.device != device or not t.is_cuda:
+    if t.dim() != 3 or not t.is_cuda or t.get_device() != index:
         raise ValueError(f"{name} must be [tokens, Hkv, d] on the CUDA device of the other tensors")
     if t.is_contiguous():
         return None
-    if t.stride(2) != 1:
+    st, sh, one = t.stride()
+    n, H, d = t.shape
+    if one != 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
     # A dimension of one element may carry any stride; it is never stepped over.
-    st = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    sh = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    return (st, sh)
+    return (st if n > 1 else H * d, sh if H > 1 else d)
+
+
+_ws_bytes = {}  # (device, sizes) -> bytes; what the library computes from the sizes and the SM count
+
+
+def _decode_fp8_bytes(index, B, Hq, Hkv, Nq, d) -> int:
+    key = (index, B, Hq, Hkv, Nq, d)
+    n = _ws_bytes.get(key)
+    if n is None:
+        with _torch().cuda.device(index):
+            n = max(fa_decode_fp8_workspace_size(B, Hq, Hkv, Nq, d), 16)
+        if len(_ws_bytes) >= 4096:
+            _ws_bytes.clear()
+        _ws_bytes[key] = n
+    return n
 
 
 def attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens=None, scale: float | None = None,
@@ -574,54 +621,56 @@ def attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens=No
     Contiguous cache: k/v [B,Nk,Hkv,d], k/v_scale float32 [B,Hkv,ceil(Nk/128)], sequence b using its
     first cache_seqlens[b] keys (int32; all Nk when None). Paged cache (block_table int32
     [B,max_pages]): k/v [num_pages,page_size,Hkv,d], k/v_scale [num_pages,Hkv], cache_seqlens
-    required. Returns O [B,Nq,Hq,d] (q's type) and L float32 [B,Hq,Nq]."""
-    import torch
-    dev = q.device
-    codes, f32, i32 = (torch.uint8, torch.float8_e4m3fn), (torch.float32,), (torch.int32,)
-    _own(q, "q", (torch.bfloat16, torch.float16), dev)
-    B, Nq, Hq, d = q.shape
+    required. `workspace`: uint8, fa_decode_fp8_workspace_size(B,Hq,Hkv,Nq,d) bytes (one is made
+    when None). Returns O [B,Nq,Hq,d] (q's type) and L float32 [B,Hq,Nq]."""
+    T = _torch()
+    f32, i32, dt = T.float32, T.int32, q.dtype
+    index = q.get_device()
+    B, Nq, Hq, d = shape = q.shape
+    if dt is not T.bfloat16 and dt is not T.float16 or index < 0 or not q.is_contiguous():
+        _own(q, "q", (T.bfloat16, T.float16), index, shape)
     n0, n1, Hkv, _ = k_cache.shape
     paged = block_table is not None
-    _own(k_cache, "k_cache", codes, dev, (n0, n1, Hkv, d) if paged else (B, n1, Hkv, d))
-    _own(v_cache, "v_cache", codes, dev, k_cache.shape)
+    kshape = (n0 if paged else B, n1, Hkv, d)
+    _codes(k_cache, "k_cache", index, kshape)
+    _codes(v_cache, "v_cache", index, kshape)
     factors = (n0, Hkv) if paged else (B, Hkv, (n1 + 127) // 128)
-    _own(k_scale, "k_scale", f32, dev, factors)
-    _own(v_scale, "v_scale", f32, dev, factors)
+    _need(k_scale, "k_scale", f32, index, factors)
+    _need(v_scale, "v_scale", f32, index, factors)
     if cache_seqlens is not None:
-        _own(cache_seqlens, "cache_seqlens", i32, dev, (B,))
-    if paged:
-        if cache_seqlens is None:
-            raise ValueError("a paged cache needs cache_seqlens")
-        _own(block_table, "block_table", i32, dev, (B, block_table.shape[1]))
+        _need(cache_seqlens, "cache_seqlens", i32, index, (B,))
+    elif paged:
+        raise ValueError("a paged cache needs cache_seqlens")
     if scale is None:
         scale = d ** -0.5
-
-    def call():
-        need = max(fa_decode_fp8_workspace_size(B, Hq, Hkv, Nq, d), 16)
-        if workspace is None:
-            ws = _temporary(lambda: torch.empty(need, dtype=torch.uint8, device=dev), dev, stream)
-        else:
-            ws = _own(workspace, "workspace", (torch.uint8,), dev)
-            if ws.numel() < need:
-                raise ValueError(f"workspace must hold {need} bytes, got {ws.numel()}")
-        o = torch.empty_like(q) if out is None else _own(out, "out", (q.dtype,), dev, q.shape)
-        L = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else \
-            _own(lse, "lse", f32, dev, (B, Hq, Nq))
-        sl = 0 if cache_seqlens is None else cache_seqlens.data_ptr()
-        if paged:
-            st = fa_decode_paged_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                                     v_scale.data_ptr(), o.data_ptr(), L.data_ptr(), sl, block_table.data_ptr(),
-                                     ws.data_ptr(), B, Hq, Hkv, Nq, n0, n1, block_table.shape[1], d, float(scale),
-                                     int(bool(causal)), _dtype_code(q), _stream(stream))
-            _check(st, "fa_decode_paged_fp8")
-        else:
-            st = fa_decode_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                               v_scale.data_ptr(), o.data_ptr(), L.data_ptr(), sl, ws.data_ptr(), B, Hq, Hkv, Nq, n1,
-                               d, float(scale), int(bool(causal)), _dtype_code(q), _stream(stream))
-            _check(st, "fa_decode_fp8")
-        return o, L
-
-    return _on(dev, call)
+    need = _decode_fp8_bytes(index, B, Hq, Hkv, Nq, d)
+    if workspace is None:
+        workspace = _temporary(T.empty(need, dtype=T.uint8, device=q.device), stream)
+    else:
+        _need(workspace, "workspace", T.uint8, index, (workspace.numel(),))
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
+    if out is None:
+        out = T.empty_like(q)
+    else:
+        _need(out, "out", dt, index, shape)
+    if lse is None:
+        lse = T.empty((B, Hq, Nq), dtype=f32, device=q.device)
+    else:
+        _need(lse, "lse", f32, index, (B, Hq, Nq))
+    sl = None if cache_seqlens is None else cache_seqlens.data_ptr()
+    code = FA_BF16 if dt is T.bfloat16 else FA_FP16
+    if paged:
+        pages = block_table.shape[-1]
+        _need(block_table, "block_table", i32, index, (B, pages))
+        _call(index, stream, "fa_decode_paged_fp8", lib().fa_decode_paged_fp8, q.data_ptr(), k_cache.data_ptr(),
+              v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), lse.data_ptr(), sl,
+              block_table.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nq, n0, n1, pages, d, scale, bool(causal), code)
+    else:
+        _call(index, stream, "fa_decode_fp8", lib().fa_decode_fp8, q.data_ptr(), k_cache.data_ptr(),
+              v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), lse.data_ptr(), sl,
+              workspace.data_ptr(), B, Hq, Hkv, Nq, n1, d, scale, bool(causal), code)
+    return out, lse
 
 
 def build_block_tables(cache_seqlens, new_lens, free_pages, block_table, page_size: int, num_pages: int,
@@ -632,46 +681,51 @@ def build_block_tables(cache_seqlens, new_lens, free_pages, block_table, page_si
     [num_free]. Returns slot_map int32 [total_new] (page * page_size + row of every packed new
     token, -1 for none), cu_new int32 [B+1], new_seqlens int32 [B] and pages_used int32 [1], the
     number of entries of free_pages taken."""
-    import torch
-    dev, i32 = new_lens.device, (torch.int32,)
-    B = new_lens.shape[0]
-    _own(new_lens, "new_lens", i32, dev, (B,))
+    T = _torch()
+    i32, index = T.int32, new_lens.get_device()
+    B, pages, num_free = new_lens.shape[0], block_table.shape[-1], free_pages.numel()
+    if index < 0 or not _fits(new_lens, i32, index, (B,)):
+        _own(new_lens, "new_lens", (i32,), index, (B,))
     if cache_seqlens is not None:
-        _own(cache_seqlens, "cache_seqlens", i32, dev, (B,))
-    _own(free_pages, "free_pages", i32, dev, (free_pages.numel(),))
-    _own(block_table, "block_table", i32, dev, (B, block_table.shape[1]))
+        _need(cache_seqlens, "cache_seqlens", i32, index, (B,))
+    _need(free_pages, "free_pages", i32, index, (num_free,))
+    _need(block_table, "block_table", i32, index, (B, pages))
+    dev = new_lens.device
+    slot_map = T.empty(total_new, dtype=i32, device=dev) if slot_map is None else \
+        _need(slot_map, "slot_map", i32, index, (total_new,))
+    cu_new = T.empty(B + 1, dtype=i32, device=dev) if cu_new is None else _need(cu_new, "cu_new", i32, index, (B + 1,))
+    new_seqlens = T.empty(B, dtype=i32, device=dev) if new_seqlens is None else \
+        _need(new_seqlens, "new_seqlens", i32, index, (B,))
+    pages_used = T.empty(1, dtype=i32, device=dev) if pages_used is None else \
+        _need(pages_used, "pages_used", i32, index, (1,))
+    _call(index, stream, "fa_build_block_tables", lib().fa_build_block_tables,
+          None if cache_seqlens is None else cache_seqlens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+          block_table.data_ptr(), slot_map.data_ptr(), cu_new.data_ptr(), new_seqlens.data_ptr(),
+          pages_used.data_ptr(), B, num_free, num_pages, page_size, pages, total_new)
+    return slot_map, cu_new, new_seqlens, pages_used
 
-    def call():
-        res = []
-        for t, name, n in ((slot_map, "slot_map", total_new), (cu_new, "cu_new", B + 1),
-                           (new_seqlens, "new_seqlens", B), (pages_used, "pages_used", 1)):
-            res.append(torch.empty(n, dtype=torch.int32, device=dev) if t is None else _own(t, name, i32, dev, (n,)))
-        st = fa_build_block_tables(0 if cache_seqlens is None else cache_seqlens.data_ptr(), new_lens.data_ptr(),
-                                   free_pages.data_ptr(), block_table.data_ptr(), *[t.data_ptr() for t in res], B,
-                                   free_pages.numel(), int(num_pages), int(page_size), block_table.shape[1],
-                                   int(total_new), _stream(stream))
-        _check(st, "fa_build_block_tables")
-        return tuple(res)
 
-    return _on(dev, call)
+def _new_rows(k_new, v_new, index):
+    ks, vs = _rows(k_new, "k_new", index), _rows(v_new, "v_new", index)
+    if v_new.shape != k_new.shape or v_new.dtype is not k_new.dtype:
+        raise ValueError("k_new and v_new must have one shape and type")
+    # Host arrays of the strides (kept alive by the caller's reference).
+    pack = ctypes.c_longlong * 2
+    return None if ks is None else pack(*ks), None if vs is None else pack(*vs)
 
 
 def cache_append_paged(k_new, v_new, k_pages, v_pages, slot_map, stream=None):
     """Rows [T,Hkv,d] of k_new and v_new (any 16-byte strides) into the 16-bit page pools
     [num_pages,page_size,Hkv,d] at slot_map int32 [T]; slots outside the pool are skipped."""
-    import torch
-    dev = k_pages.device
-    ks, vs = _rows(k_new, "k_new", dev), _rows(v_new, "v_new", dev)
-    T, Hkv, d = k_new.shape
-    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
-        raise ValueError("k_new and v_new must have one shape and type")
+    index = k_pages.get_device()
+    ks, vs = _new_rows(k_new, v_new, index)
+    n_new, Hkv, d = k_new.shape
     n, page = k_pages.shape[:2]
-    _own(k_pages, "k_pages", (k_new.dtype,), dev, (n, page, Hkv, d))
-    _own(v_pages, "v_pages", (k_new.dtype,), dev, (n, page, Hkv, d))
-    _own(slot_map, "slot_map", (torch.int32,), dev, (T,))
-    _check(_on(dev, lambda: fa_cache_append_paged(
-        k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_pages.data_ptr(), v_pages.data_ptr(), slot_map.data_ptr(), T,
-        Hkv, n, page, d, _dtype_code(k_new), _stream(stream))), "fa_cache_append_paged")
+    _need(k_pages, "k_pages", k_new.dtype, index, (n, page, Hkv, d))
+    _need(v_pages, "v_pages", k_new.dtype, index, (n, page, Hkv, d))
+    _need(slot_map, "slot_map", _torch().int32, index, (n_new,))
+    _call(index, stream, "fa_cache_append_paged", lib().fa_cache_append_paged, k_new.data_ptr(), v_new.data_ptr(), ks,
+          vs, k_pages.data_ptr(), v_pages.data_ptr(), slot_map.data_ptr(), n_new, Hkv, n, page, d, _dtype_code(k_new))
 
 
 def cache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cu_new, cache_seqlens, new_seqlens,
@@ -681,31 +735,30 @@ def cache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cu_new, c
     Sequence b's rows cu_new[b].. become its positions cache_seqlens[b] .. new_seqlens[b]-1 (int32
     tensors, as build_block_tables gives them), at most max_new of them. Caches and factors:
     the layouts of attention_decode_fp8 (paged with block_table), written in place."""
-    import torch
-    dev = k_cache.device
-    codes, f32, i32 = (torch.uint8, torch.float8_e4m3fn), (torch.float32,), (torch.int32,)
-    ks, vs = _rows(k_new, "k_new", dev), _rows(v_new, "v_new", dev)
-    T, Hkv, d = k_new.shape
-    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
-        raise ValueError("k_new and v_new must have one shape and type")
+    T = _torch()
+    f32, i32 = T.float32, T.int32
+    index = k_cache.get_device()
+    ks, vs = _new_rows(k_new, v_new, index)
+    n_new, Hkv, d = k_new.shape
     B = cache_seqlens.shape[0]
     n0, n1 = k_cache.shape[:2]
     paged = block_table is not None
-    _own(k_cache, "k_cache", codes, dev, (n0 if paged else B, n1, Hkv, d))
-    _own(v_cache, "v_cache", codes, dev, k_cache.shape)
+    kshape = (n0 if paged else B, n1, Hkv, d)
+    _codes(k_cache, "k_cache", index, kshape)
+    _codes(v_cache, "v_cache", index, kshape)
     factors = (n0, Hkv) if paged else (B, Hkv, (n1 + 127) // 128)
-    _own(k_scale, "k_scale", f32, dev, factors)
-    _own(v_scale, "v_scale", f32, dev, factors)
-    _own(cu_new, "cu_new", i32, dev, (B + 1,))
-    _own(cache_seqlens, "cache_seqlens", i32, dev, (B,))
-    _own(new_seqlens, "new_seqlens", i32, dev, (B,))
+    _need(k_scale, "k_scale", f32, index, factors)
+    _need(v_scale, "v_scale", f32, index, factors)
+    _need(cu_new, "cu_new", i32, index, (B + 1,))
+    _need(cache_seqlens, "cache_seqlens", i32, index, (B,))
+    _need(new_seqlens, "new_seqlens", i32, index, (B,))
     head = (k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), cu_new.data_ptr(), cache_seqlens.data_ptr(), new_seqlens.data_ptr())
     if paged:
-        _own(block_table, "block_table", i32, dev, (B, block_table.shape[1]))
-        _check(_on(dev, lambda: fa_cache_append_paged_fp8(
-            *head, block_table.data_ptr(), B, T, int(max_new), Hkv, n0, n1, block_table.shape[1], d,
-            _dtype_code(k_new), _stream(stream))), "fa_cache_append_paged_fp8")
+        pages = block_table.shape[-1]
+        _need(block_table, "block_table", i32, index, (B, pages))
+        _call(index, stream, "fa_cache_append_paged_fp8", lib().fa_cache_append_paged_fp8, *head,
+              block_table.data_ptr(), B, n_new, max_new, Hkv, n0, n1, pages, d, _dtype_code(k_new))
     else:
-        _check(_on(dev, lambda: fa_cache_append_fp8(*head, B, T, int(max_new), Hkv, n1, d, _dtype_code(k_new),
-                                                    _stream(stream))), "fa_cache_append_fp8")
+        _call(index, stream, "fa_cache_append_fp8", lib().fa_cache_append_fp8, *head, B, n_new, max_new, Hkv, n1, d,
+              _dtype_code(k_new))

@@ -12,10 +12,12 @@ namespace fa {
 //     need_b = ceil((n_b + c_b) / ps) - ceil(n_b / ps)
 // pages; two exclusive prefix sums over b give the first of its pages in the free
 // list and the first of its tokens in the packed order. Every CTA takes the whole
-// scan itself (B integers, a few block scans), then writes its own slice of the slot
-// map and the table rows of its own requests: one launch, no CTA waits for another.
-// What bounds it is latency (one read of the lengths, the scan, one dependent page
-// read, one write).
+// scan itself (B integers, a few block scans), then writes its share of the new table
+// entries and its slice of the slot map, finding the request of an entry or token in
+// the scanned sums by bisection: one launch, no CTA waits for another, and a request's
+// pages are spread over the threads however many they are (a warp per request, one
+// request after the other, took 11.8 us for 256 requests). What bounds it is latency:
+// one read of the lengths, the scan, one dependent page read, one write.
 struct TableArgs {
     const int* seqlens;    // [B] or null (0)
     const int* new_lens;   // [B]
@@ -30,40 +32,48 @@ struct TableArgs {
 };
 
 constexpr int kTableThreads = 256;
-constexpr int kTableSlice = 1024;  // tokens of the slot map a CTA writes
+constexpr int kTableRun = 4;  // consecutive tokens of a thread
+constexpr int kTableSlice = kTableThreads * kTableRun;  // tokens of the slot map a CTA writes
 
-// The page of rank j (0-based) of a request: one it holds already, or one of the free
-// list from `first` on.
-__device__ __forceinline__ int table_page(const TableArgs& a, int b, int j, int have, long long first) {
-    return j < have ? a.block_table[static_cast<size_t>(b) * a.max_pages + j] : a.free_pages[first + (j - have)];
+// The last entry of the ascending sums[0 .. n) that is at most x (sums[0] <= x): of equal
+// ones that is the only request with anything of its own there.
+__device__ __forceinline__ int table_find(const int* sums, int n, int x) {
+    int l = 0, r = n - 1;
+    while (l < r) {
+        const int m = (l + r + 1) >> 1;
+        if (sums[m] <= x) l = m;
+        else r = m - 1;
+    }
+    return l;
 }
 
 __global__ void __launch_bounds__(kTableThreads) fa_block_tables_kernel(const TableArgs a) {
     constexpr int kWarps = kTableThreads / 32;
     __shared__ long long w_tok[kWarps], w_page[kWarps];
-    __shared__ int s_tok[kTableThreads + 1];    // first packed token of the chunk's requests
-    __shared__ int s_old[kTableThreads];        // tokens cached; -1: the request gets nothing
-    __shared__ long long s_first[kTableThreads];  // its first page in the free list
+    __shared__ int s_tok[kTableThreads + 1];   // first packed token of the chunk's requests
+    __shared__ int s_page[kTableThreads];      // their first page in the free list
+    __shared__ int s_old[kTableThreads];       // tokens cached; -1: the request gets nothing
     const int tid = static_cast<int>(threadIdx.x), lane = lane_id(), warp = warp_id();
-    const int cta = static_cast<int>(blockIdx.x);
-    const long long t_lo = static_cast<long long>(cta) * kTableSlice;
-    const long long t_hi = min(t_lo + kTableSlice, static_cast<long long>(a.total_new));
-    const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
+    const int cta = static_cast<int>(blockIdx.x), G = static_cast<int>(gridDim.x);
+    const uint32_t ps = static_cast<uint32_t>(a.page_size);
+    const long long cap = static_cast<long long>(a.max_pages) * a.page_size;  // < 2^31
+    const int t_lo = cta * kTableSlice;  // < total_new + 2^10
+    const int t_hi = static_cast<int>(min(static_cast<long long>(t_lo) + kTableSlice, static_cast<long long>(a.total_new)));
+    const bool aligned = (reinterpret_cast<uintptr_t>(a.slot_map) & 15u) == 0;
+    auto pages_of = [ps](int n) { return static_cast<int>((static_cast<uint32_t>(n) + ps - 1) / ps); };
     long long tok = 0, page = 0;  // packed tokens and pages of the chunks before
-    int chunk = 0;
     bool bad = false;
-    long long used = 0;  // pages of the requests this thread accepted, counted from the list's start
-    for (int base = 0; base < a.B; base += kTableThreads, ++chunk) {
+    int used = 0;  // pages of the requests this thread accepted, counted from the list's start
+    for (int base = 0, chunk = 0; base < a.B; base += kTableThreads, ++chunk) {
         const int b = base + tid;
-        long long n = 0, c = 0;
+        int n = 0, c = 0;
         if (b < a.B) {
             n = a.seqlens ? a.seqlens[b] : 0;
             c = a.new_lens[b];
         }
-        bool ok = n >= 0 && c >= 0 && n + c <= cap;
-        c = max(c, 0LL);
-        const int have = ok ? static_cast<int>((n + a.page_size - 1) / a.page_size) : 0;
-        const int need = ok ? static_cast<int>((n + c + a.page_size - 1) / a.page_size) - have : 0;
+        bool ok = n >= 0 && c >= 0 && static_cast<long long>(n) + c <= cap;
+        c = max(c, 0);
+        const int need = ok ? pages_of(n + c) - pages_of(n) : 0;
         long long it = c, ip = need;  // inclusive sums over the warp, then the block
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -93,71 +103,88 @@ __global__ void __launch_bounds__(kTableThreads) fa_block_tables_kernel(const Ta
         // map ends, every later request that needs more of it is refused too.
         ok = ok && tok0 + c <= a.total_new && (need == 0 || page0 + need <= a.num_free);
         s_tok[tid] = static_cast<int>(min(tok0, static_cast<long long>(a.total_new)));
-        s_old[tid] = ok ? static_cast<int>(n) : -1;
-        s_first[tid] = page0;
-        if (b < a.B) {
-            bad |= !ok;
-            if (ok && need > 0) used = page0 + need;
-            if (chunk % static_cast<int>(gridDim.x) == cta) {
-                a.cu_new[b] = s_tok[tid];
-                a.new_seqlens[b] = static_cast<int>(ok ? n + c : n);
-            }
-        }
+        s_page[tid] = static_cast<int>(min(page0, static_cast<long long>(a.num_free)));
+        s_old[tid] = ok ? n : -1;
         tok += tt;
         page += tp;
         if (tid == 0) s_tok[kTableThreads] = static_cast<int>(min(tok, static_cast<long long>(a.total_new)));
         __syncthreads();
-        // Table rows of this CTA's requests: a warp for each, its lanes over the new pages.
-        const int here = min(kTableThreads, a.B - base);
-        if (chunk % static_cast<int>(gridDim.x) == cta) {
-            for (int i = warp; i < here; i += kWarps) {
-                if (s_old[i] < 0) continue;
-                const int old = s_old[i];
-                const int count = s_tok[i + 1] - s_tok[i];
-                const int h0 = (old + a.page_size - 1) / a.page_size;
-                const int h1 = static_cast<int>((static_cast<long long>(old) + count + a.page_size - 1) / a.page_size);
-                for (int j = h0 + lane; j < h1; j += 32)
-                    a.block_table[static_cast<size_t>(base + i) * a.max_pages + j] = a.free_pages[s_first[i] + j - h0];
+        if (b < a.B) {
+            bad |= !ok;
+            if (ok && need > 0) used = static_cast<int>(page0) + need;
+            if (chunk % G == cta) {
+                a.cu_new[b] = s_tok[tid];
+                a.new_seqlens[b] = ok ? n + c : n;
             }
         }
-        // Slots of the tokens of this CTA's slice that belong to the chunk's requests.
-        const int lo = static_cast<int>(max(t_lo, static_cast<long long>(s_tok[0])));
-        const int hi = static_cast<int>(min(t_hi, static_cast<long long>(s_tok[here])));
-        for (int t = lo + tid; t < hi; t += kTableThreads) {
-            int l = 0, r = here - 1;  // the last request that starts at or before t (not an empty one)
-            while (l < r) {
-                const int m = (l + r + 1) / 2;
-                if (s_tok[m] <= t) l = m;
-                else r = m - 1;
-            }
-            int slot = -1;
-            if (s_old[l] >= 0) {
+        const int here = min(kTableThreads, a.B - base);
+        // New table entries: entry i of the free list belongs to the request whose pages start
+        // at or before it.
+        const int p_end = static_cast<int>(min(page, static_cast<long long>(a.num_free)));
+        for (long long i = static_cast<long long>(s_page[0]) + cta * kTableThreads + tid; i < p_end;
+             i += static_cast<long long>(G) * kTableThreads) {
+            const int pg = a.free_pages[i];
+            const int l = table_find(s_page, here, static_cast<int>(i));
+            if (s_old[l] >= 0)
+                a.block_table[static_cast<size_t>(base + l) * a.max_pages + pages_of(s_old[l]) + (i - s_page[l])] = pg;
+        }
+        // Slots of the tokens of this CTA's slice that belong to the chunk's requests, runs
+        // of consecutive tokens a thread: their request and page change seldom.
+        const int lo = max(t_lo, s_tok[0]), hi = min(t_hi, s_tok[here]);
+        const int t0 = t_lo + tid * kTableRun;
+        if (t0 < hi && t0 + kTableRun > lo) {
+            int slot[kTableRun];
+            int l = table_find(s_tok, here, max(t0, lo));
+            int at = -1, pg = -1;  // the page's place in the request's row, the page
+#pragma unroll
+            for (int k = 0; k < kTableRun; ++k) {
+                const int t = t0 + k;
+                slot[k] = -1;
+                if (t < lo || t >= hi) continue;
+                while (l + 1 < here && s_tok[l + 1] <= t) {
+                    ++l;
+                    at = -1;
+                }
                 const int old = s_old[l];
+                if (old < 0) continue;
                 const int pos = old + (t - s_tok[l]);
-                const int have_l = (old + a.page_size - 1) / a.page_size;
-                const int pg = table_page(a, base + l, pos / a.page_size, have_l, s_first[l]);
-                if (pg >= 0 && pg < a.num_pages) slot = pg * a.page_size + pos % a.page_size;
+                const int j = static_cast<int>(static_cast<uint32_t>(pos) / ps);
+                if (j != at) {
+                    const int have = pages_of(old);
+                    pg = j < have ? a.block_table[static_cast<size_t>(base + l) * a.max_pages + j]
+                                  : a.free_pages[s_page[l] + (j - have)];
+                    at = j;
+                }
+                if (pg >= 0 && pg < a.num_pages) slot[k] = pg * a.page_size + (pos - j * a.page_size);
                 else bad = true;
             }
-            a.slot_map[t] = slot;
+            if (aligned && t0 >= lo && t0 + kTableRun <= hi) {
+                *reinterpret_cast<int4*>(a.slot_map + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kTableRun; ++k)
+                    if (t0 + k >= lo && t0 + k < hi) a.slot_map[t0 + k] = slot[k];
+            }
         }
-        __syncthreads();
+        if (base + kTableThreads < a.B) __syncthreads();  // the sums are written again
     }
     // Tokens of no request.
-    for (long long t = max(t_lo, min(tok, static_cast<long long>(a.total_new))) + tid; t < t_hi; t += kTableThreads)
+    for (long long t = max(static_cast<long long>(t_lo), min(tok, static_cast<long long>(a.total_new))) + tid; t < t_hi;
+         t += kTableThreads)
         a.slot_map[t] = -1;
+    if (bad) atomicCAS(a.err, 0, kErrCacheRange);
+    if (cta != 0) return;
     // The accepted requests that take pages are a prefix of those that need any, so the
     // largest count is the number of pages taken.
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) used = max(used, __shfl_xor_sync(0xffffffffu, used, off));
+    used = __reduce_max_sync(0xffffffffu, used);
+    __syncthreads();
     if (lane == 0) w_page[warp] = used;
     __syncthreads();
-    if (cta == 0 && tid == 0) {
-        for (int w = 1; w < kWarps; ++w) used = max(used, w_page[w]);
-        a.pages_used[0] = static_cast<int>(used);
+    if (tid == 0) {
+        for (int w = 1; w < kWarps; ++w) used = max(used, static_cast<int>(w_page[w]));
+        a.pages_used[0] = used;
         a.cu_new[a.B] = static_cast<int>(min(tok, static_cast<long long>(a.total_new)));
     }
-    if (bad) atomicCAS(a.err, 0, kErrCacheRange);
 }
 
 // ------------------------------------------------------------------ 16-bit append
@@ -204,8 +231,10 @@ __global__ void __launch_bounds__(256) fa_append16_kernel(const Append16Args a) 
 //
 // One group of TG threads takes one (block, KV head, key or value): it reads the new
 // rows once, holding them in registers (16 bytes a chunk, kHold chunks a thread) for
-// the maximum and the codes. TG = 32 where a block's new rows fit a warp's registers
-// (eight groups share a CTA, no block barrier), else 256.
+// the maximum and the codes. TG is the smallest of 32, 64, 128 and 256 whose registers
+// hold the rows a block can get, so that every thread has kHold loads in flight (what
+// bounds it is their latency: 256 threads for 64-row blocks, four loads each, took 45 us
+// for 18,000 tokens of 8 heads). Groups of a warp share CTAs of eight.
 struct Append8Args {
     const uint16_t* x[2];  // k, v
     uint8_t* codes[2];
@@ -270,13 +299,13 @@ __device__ __forceinline__ uint32_t rescale4_e4m3(uint32_t c, float ratio) {
 }
 
 template <bool BF16, int D, int TG>
-__global__ void __launch_bounds__(256) fa_append8_kernel(const Append8Args a) {
+__global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 4 : 1024 / TG) fa_append8_kernel(const Append8Args a) {
     constexpr int kChunks = D / 8;            // 16-byte chunks of a row
     constexpr int kRows = TG / kChunks;       // rows a group reads at a time
     __shared__ float red[8];
     const int lane = lane_id(), warp = warp_id();
-    const long long grp = static_cast<long long>(blockIdx.x) * (256 / TG) + (TG == 32 ? warp : 0);
-    if (grp >= a.groups) return;  // TG = 256: uniform over the CTA
+    const long long grp = TG == 32 ? static_cast<long long>(blockIdx.x) * 8 + warp : blockIdx.x;
+    if (grp >= a.groups) return;  // uniform over the group
     const int tg = TG == 32 ? lane : static_cast<int>(threadIdx.x);
     // Heads fastest (a row's heads lie together), then key / value, block, sequence.
     const int h = static_cast<int>(grp % a.Hkv);
@@ -297,6 +326,15 @@ __global__ void __launch_bounds__(256) fa_append8_kernel(const Append8Args a) {
     if (p0 >= p1) return;
     const int r0 = static_cast<int>(p0 - static_cast<long long>(blk) * a.unit);  // first new row of the block
     const int rows = static_cast<int>(p1 - p0);
+    // The rows are on their way before the block's place is looked up.
+    const uint16_t* src = a.x[kv] + (t0 + p0 - old) * a.st[kv] + h * a.sh[kv];
+    const int c = tg % kChunks, r_first = tg / kChunks;
+    uint4 held[kHold];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        const int r = r_first + i * kRows;
+        if (r < rows) held[i] = *reinterpret_cast<const uint4*>(src + r * a.st[kv] + c * 8);
+    }
     const int per_row = a.Hkv * D;
     uint8_t* dst;  // row 0 of the block, this head
     float* fac;
@@ -312,10 +350,7 @@ __global__ void __launch_bounds__(256) fa_append8_kernel(const Append8Args a) {
         dst = a.codes[kv] + (static_cast<size_t>(b) * a.cap + static_cast<size_t>(blk) * a.unit) * per_row + h * D;
         fac = a.factors[kv] + (static_cast<size_t>(b) * a.Hkv + h) * a.per_seq + blk;
     }
-    const uint16_t* src = a.x[kv] + (t0 + p0 - old) * a.st[kv] + h * a.sh[kv];
-    const int c = tg % kChunks, r_first = tg / kChunks;
     const float f_old = r0 > 0 ? *fac : 0.f;
-    uint4 held[kHold];
     float amax = 0.f;
     auto take = [&](const uint4& u) {
         float f[8];
@@ -327,11 +362,6 @@ __global__ void __launch_bounds__(256) fa_append8_kernel(const Append8Args a) {
         }
     };
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        const int r = r_first + i * kRows;
-        if (r < rows) held[i] = *reinterpret_cast<const uint4*>(src + r * a.st[kv] + c * 8);
-    }
-#pragma unroll
     for (int i = 0; i < kHold; ++i)
         if (r_first + i * kRows < rows) take(held[i]);
     // Blocks past the registers' reach (pages of more than kHold * kRows rows): read twice.
@@ -339,11 +369,11 @@ __global__ void __launch_bounds__(256) fa_append8_kernel(const Append8Args a) {
         take(*reinterpret_cast<const uint4*>(src + r * a.st[kv] + c * 8));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    if constexpr (TG == 256) {
+    if constexpr (TG > 32) {
         if (lane == 0) red[warp] = amax;
         __syncthreads();  // every thread has read the old factor too
 #pragma unroll
-        for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[w]);
+        for (int w = 0; w < TG / 32; ++w) amax = fmaxf(amax, red[w]);
     }
     const int e = e4m3_exponent(amax);
     const float f_new = fmaxf(exp2_int(e), f_old);

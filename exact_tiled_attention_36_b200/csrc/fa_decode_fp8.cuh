@@ -324,18 +324,11 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     constexpr int D = PAIR ? 64 : 128;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (!smem_base_ok(smem, args.err)) return;
-    asm volatile("griddepcontrol.launch_dependents;");
     const int cta = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
     const int warp = warp_id(), lane = lane_id();
     uint8_t* misc = smem + C::kMiscOff;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
     int* abort_flag = reinterpret_cast<int*>(misc + 4);
-    // TMEM first: the SM starts its second CTA only after the first gave up the permit to
-    // allocate (measured: 0.35 us after it, wherever in the kernel that is).
-    if (warp == 1) {
-        tmem_alloc(tmem_holder, C::kTmemCols);
-        tmem_relinquish();
-    }
     uint8_t* sQ = smem + C::kQOff;
     uint8_t* sP = smem + C::kPOff;
     uint8_t* ring = smem + C::kRingOff;
@@ -386,6 +379,17 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
+    }
+    // Launched as a programmatic dependent of whatever ran before on the stream: what
+    // follows reads that kernel's results (and overwrites the workspace).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The merge may be scheduled now; it waits for this grid in turn.
+    asm volatile("griddepcontrol.launch_dependents;");
+    // TMEM first: the SM starts its second CTA only after the first gave up the permit to
+    // allocate (measured: 0.35 us after it, wherever in the kernel that is).
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, C::kTmemCols);
+        tmem_relinquish();
     }
     Dec8Range rg;
     const bool work = dec8_locate<THREADS>(args, misc, rg);
@@ -879,6 +883,7 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
     // Launched as a programmatic dependent of the split kernel: what that wrote may be read
     // from here on.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int2 cc = a.meta[item];  // of an item without keys: anything
     const int len = dec8_len(a, b);
     const int c0 = cc.x, c1 = len > 0 ? cc.y : cc.x - 1;

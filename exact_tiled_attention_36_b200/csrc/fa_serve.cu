@@ -44,12 +44,16 @@ fa_status append_checks(const void* k, const void* v, const void* kc, const void
     return FA_OK;
 }
 
+// `chunks`: pieces of 8 values that a block's new rows of one head can have.
 template <bool BF16, int D>
-fa_status launch_append8(const fa::Append8Args& a, bool narrow, cudaStream_t s) {
-    const long long ctas = narrow ? (a.groups + 7) / 8 : a.groups;
+fa_status launch_append8(const fa::Append8Args& a, long long chunks, cudaStream_t s) {
+    const bool warps = chunks <= 32 * fa::kHold;
+    const long long ctas = warps ? (a.groups + 7) / 8 : a.groups;
     if (ctas > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     const unsigned grid = static_cast<unsigned>(ctas);
-    if (narrow) fa::fa_append8_kernel<BF16, D, 32><<<grid, 256, 0, s>>>(a);
+    if (warps) fa::fa_append8_kernel<BF16, D, 32><<<grid, 256, 0, s>>>(a);
+    else if (chunks <= 64 * fa::kHold) fa::fa_append8_kernel<BF16, D, 64><<<grid, 64, 0, s>>>(a);
+    else if (chunks <= 128 * fa::kHold) fa::fa_append8_kernel<BF16, D, 128><<<grid, 128, 0, s>>>(a);
     else fa::fa_append8_kernel<BF16, D, 256><<<grid, 256, 0, s>>>(a);
     return launched();
 }
@@ -96,12 +100,10 @@ fa_status append8(const void* k, const void* v, const long long* k_strides, cons
     a.groups = static_cast<long long>(B) * a.touched * Hkv * 2;
     a.err = fa_host::error_word();
     if (!a.err) return FA_ERR_CUDA;
-    // A warp holds kHold chunks of 8 values a lane: the rows of a block that this call can
-    // bring decide whether a warp's registers take them.
-    const bool narrow = static_cast<long long>(a.max_new < unit ? a.max_new : unit) * (d / 8) <= 32 * fa::kHold;
+    const long long chunks = static_cast<long long>(a.max_new < unit ? a.max_new : unit) * (d / 8);
     const cudaStream_t s = cu(stream);
-    if (dtype == FA_BF16) return d == 64 ? launch_append8<true, 64>(a, narrow, s) : launch_append8<true, 128>(a, narrow, s);
-    return d == 64 ? launch_append8<false, 64>(a, narrow, s) : launch_append8<false, 128>(a, narrow, s);
+    if (dtype == FA_BF16) return d == 64 ? launch_append8<true, 64>(a, chunks, s) : launch_append8<true, 128>(a, chunks, s);
+    return d == 64 ? launch_append8<false, 64>(a, chunks, s) : launch_append8<false, 128>(a, chunks, s);
 }
 
 // How a call's rows become items, and its workspace: meta (each item's first and last CTA), the
@@ -152,26 +154,30 @@ bool kernel_ready(int smem) {
 template <bool BF16, int D, bool PAGED, int RT>
 fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode8Args& a, int causal,
                         bool run_split, cudaStream_t s) {
+    // Both kernels launch as programmatic dependents of the one before them on the stream: the
+    // launch and the part before their griddepcontrol.wait overlap its end.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (run_split) {
         constexpr auto kern = fa::fa_decode8_kernel<BF16, D == 64, PAGED, RT>;
         using C = fa::Dec8Cfg<BF16, D == 64, RT>;
         if (!kernel_ready<kern>(C::kSmemBytes)) return FA_ERR_CUDA;
-        kern<<<a.G, C::kThreads, C::kSmemBytes, s>>>(mk, mv, a, causal);
-        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+        cfg.gridDim = dim3(a.G);
+        cfg.blockDim = dim3(C::kThreads);
+        cfg.dynamicSmemBytes = C::kSmemBytes;
+        if (cudaLaunchKernelEx(&cfg, kern, mk, mv, a, causal) != cudaSuccess) return FA_ERR_CUDA;
     }
-    // The merge is a programmatic dependent of the split kernel (griddepcontrol.wait in it).
-    cudaLaunchConfig_t cfg{};
     // A row's segments: about CTAs / items, one or two more where ranges cross.
     const int rows = a.B * a.Hq * a.Nq;
     const bool wide = a.G > 6LL * a.B * a.HV;
     cfg.gridDim = dim3(wide ? rows : (rows + 3) / 4);
     cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = run_split ? 1 : 0;
+    cfg.dynamicSmemBytes = 0;
     if ((wide ? cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT, true>, a, rows)
               : cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT, false>, a, rows)) != cudaSuccess)
         return FA_ERR_CUDA;
@@ -291,6 +297,7 @@ fa_status fa_build_block_tables(const int* cache_seqlens, const int* new_lens, c
     if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL ||
         static_cast<long long>(max_pages) * page_size > 0x7fffffffLL)
         return FA_ERR_UNSUPPORTED;  // a slot is an int32
+    if (total_new > 0x7fffffff - 2 * fa::kTableSlice) return FA_ERR_UNSUPPORTED;
     fa::TableArgs a{};
     a.seqlens = cache_seqlens;
     a.new_lens = new_lens;
@@ -308,9 +315,7 @@ fa_status fa_build_block_tables(const int* cache_seqlens, const int* new_lens, c
     a.total_new = total_new;
     a.err = fa_host::error_word();
     if (!a.err) return FA_ERR_CUDA;
-    const int by_tokens = (total_new + fa::kTableSlice - 1) / fa::kTableSlice;
-    const int by_requests = (B + fa::kTableThreads - 1) / fa::kTableThreads;
-    const int grid = by_tokens > by_requests ? by_tokens : by_requests;
+    const int grid = total_new > fa::kTableSlice ? (total_new + fa::kTableSlice - 1) / fa::kTableSlice : 1;
     fa::fa_block_tables_kernel<<<grid, fa::kTableThreads, 0, cu(stream)>>>(a);
     return launched();
 }

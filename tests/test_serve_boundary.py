@@ -148,21 +148,24 @@ def test_row_strides_of_views():
     meta = torch.zeros(5, 3, 2, 64, dtype=torch.bfloat16)
 
     class Fake:  # a CUDA tensor's shape and strides on a machine without one
-        is_cuda, device = True, "cuda:0"
+        is_cuda = True
 
         def __init__(self, t):
             self.t = t
 
+        def get_device(self):
+            return 0
+
         def __getattr__(self, name):
             return getattr(self.t, name)
 
-    assert fb._rows(Fake(meta[:, 0]), "k", "cuda:0") == (384, 64)
-    assert fb._rows(Fake(meta[:, 0].contiguous()), "k", "cuda:0") is None
-    assert fb._rows(Fake(meta[:, 0, :1]), "k", "cuda:0") == (384, 64)
+    assert fb._rows(Fake(meta[:, 0]), "k", 0) == (384, 64)
+    assert fb._rows(Fake(meta[:, 0].contiguous()), "k", 0) is None
+    assert fb._rows(Fake(meta[:, 0, :1]), "k", 0) == (384, 64)
     with pytest.raises(ValueError, match="contiguous"):
-        fb._rows(Fake(meta[:, 0].transpose(1, 2)), "k", "cuda:0")
+        fb._rows(Fake(meta[:, 0].transpose(1, 2)), "k", 0)
     with pytest.raises(ValueError, match="tokens"):
-        fb._rows(Fake(meta), "k", "cuda:0")
+        fb._rows(Fake(meta), "k", 0)
 
 
 # The references themselves, against torch and by hand.
