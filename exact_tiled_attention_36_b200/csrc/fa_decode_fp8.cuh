@@ -75,6 +75,8 @@ struct Dec8Cfg {
     static constexpr int RH = PAIR ? RT / 2 : RT;                 // rows of one KV head
     static constexpr int NH = (NT * RH + 15) / 16 * 16;           // rows of Q of one KV head
     static constexpr int NQ = PAIR ? 2 * NH : NH;
+    static constexpr int kRowPieces = PAIR ? 8 : 16;              // 8-value pieces of a query row
+    static constexpr int kQPieces = RT * kRowPieces;
     static constexpr int kTile = 128 * 128;                       // one K or V tile
     static constexpr int kUnits = 5;                              // ring of tiles: K, V, K, V, ...
     static constexpr int kQB = 2;                                 // query buffers
@@ -95,6 +97,7 @@ struct Dec8Cfg {
     static constexpr uint32_t kColO = 2 * NQ;                     // S^T buffers at 0 and NQ
     static constexpr uint32_t kCols = 2 * NQ + 2 * N;
     static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
+    static_assert(kQPieces <= 128 * NW && kQPieces % 32 == 0, "one piece a softmax thread, whole warps");
     static_assert(kCols <= 256, "two CTAs share the SM's 512 columns");
     static_assert(kRingOff % 1024 == 0 && kPOff % 1024 == 0, "swizzle atoms");
     static_assert(kSmemBytes <= 115712, "two CTAs share the SM's shared memory");
@@ -311,6 +314,50 @@ __device__ __forceinline__ void e4m3_terms(uint32_t x, uint32_t (&c)[NT]) {
         c[i] = e4m3x2_of_h2(x);
         if (i + 1 < NT) x = h2_rest(x, h2_of_e4m3x2(c[i]));
     }
+}
+
+// The queries' terms: piece i of a tile's RT rows is 8 values, consecutive pieces (and
+// lanes) one row's. dec8_query_load reads it (zeros where the row is none of the item's),
+// dec8_query_put scales the row by a power of two so that its largest magnitude is below
+// 448, writes the piece's terms and the row's scale. Whole warps call them.
+template <typename C, bool PAIR, int RT>
+__device__ __forceinline__ uint4 dec8_query_load(const Decode8Args& a, const Dec8Item& it, int i) {
+    const int r = i / C::kRowPieces, c = i % C::kRowPieces;
+    const int hh = it.vh / a.nch, ch = it.vh % a.nch;
+    const int hd = PAIR ? r / C::RH : 0, rr = PAIR ? r % C::RH : r;
+    const int gr = ch * a.RC + rr, head = PAIR ? 2 * hh + hd : hh;
+    if (rr >= a.RC || gr >= a.R || head >= a.Hkv) return make_uint4(0, 0, 0, 0);
+    const size_t row = (static_cast<size_t>(it.b) * a.Nq + gr / a.group) * a.Hq + static_cast<size_t>(head) * a.group +
+                       gr % a.group;
+    return *reinterpret_cast<const uint4*>(a.q + (row * C::kRowPieces + c) * 8);
+}
+template <typename C, bool BF16, bool PAIR, int RT>
+__device__ __forceinline__ void dec8_query_put(const Decode8Args& a, const uint4& raw, int i, uint8_t* dst, float* qf) {
+    constexpr int NT = C::NT;
+    const int r = i / C::kRowPieces, c = i % C::kRowPieces;
+    const int hd = PAIR ? r / C::RH : 0, rr = PAIR ? r % C::RH : r;
+    float v[8];
+    unpack8<BF16>(raw, v);
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
+#pragma unroll
+    for (int off = C::kRowPieces / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const int e = e4m3_exponent(top);
+    const float inv = exp2_int(-e);
+    uint32_t t4[4][NT];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < INFINITY ? v[k] * inv : __uint_as_float(0x7fffffffu);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e4m3_terms<NT>(pack2<false>(v[2 * k], v[2 * k + 1]), t4[k]);
+    const int col = hd * 64 + c * 8;  // the piece's first byte of the tile's row
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int row = hd * C::NH + t * C::RH + rr;
+        *reinterpret_cast<uint2*>(dst + row * 128 + (((col >> 4) ^ (row & 7)) << 4) + (col & 15)) =
+            make_uint2(t4[0][t] | (t4[1][t] << 16), t4[2][t] | (t4[3][t] << 16));
+    }
+    if (c == 0) qf[r] = a.scale_log2 * exp2_int(e);
 }
 
 // ------------------------------------------------------------------- split kernel
@@ -567,57 +614,20 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
-            const int hh = it.vh / args.nch, ch = it.vh % args.nch;
-            // CPR lanes hold a row, 8 values each; RPI rows at a time.
-            constexpr int CPR = D / 8, RPI = 32 / CPR, NI = RT / RPI;
-            const int c = lane % CPR;
-            uint4 raw[NI];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int r = i * RPI + lane / CPR;
-                const int hd = PAIR ? r / RH : 0, rr = PAIR ? r % RH : r;
-                const int gr = ch * args.RC + rr;
-                const int head = PAIR ? 2 * hh + hd : hh;
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (rr < args.RC && gr < args.R && head < args.Hkv) {
-                    const size_t row = (static_cast<size_t>(it.b) * args.Nq + gr / args.group) * args.Hq +
-                                       static_cast<size_t>(head) * args.group + gr % args.group;
-                    raw[i] = *reinterpret_cast<const uint4*>(args.q + row * D + c * 8);
-                }
-            }
             const int qb = nq % QB;
-            if (!(ok = warp_all(mbar_wait(&q_empty[qb], ((nq / QB) & 1) ^ 1u, wc, 127)))) break;
-            uint8_t* dst = sQ + qb * C::NQ * 128;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int r = i * RPI + lane / CPR;
-                const int hd = PAIR ? r / RH : 0, rr = PAIR ? r % RH : r;
-                float v[8];
-                unpack8<BF16>(raw[i], v);
-                float top = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
-#pragma unroll
-                for (int off = CPR / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const int e = e4m3_exponent(top);
-                const float inv = exp2_int(-e);
-                uint32_t t4[4][NT];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < INFINITY ? v[k] * inv : __uint_as_float(0x7fffffffu);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) e4m3_terms<NT>(pack2<false>(v[2 * k], v[2 * k + 1]), t4[k]);
-                const int col = hd * 64 + c * 8;  // this lane's first byte of the row
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const int row = hd * C::NH + t * RH + rr;
-                    *reinterpret_cast<uint2*>(dst + row * 128 + (((col >> 4) ^ (row & 7)) << 4) + (col & 15)) =
-                        make_uint2(t4[0][t] | (t4[1][t] << 16), t4[2][t] | (t4[3][t] << 16));
+            if (nq > 0) {  // the first segment's: the softmax warps
+                uint4 raw = dec8_query_load<C, PAIR, RT>(args, it, lane);
+                if (!(ok = warp_all(mbar_wait(&q_empty[qb], ((nq / QB) & 1) ^ 1u, wc, 127)))) break;
+#pragma unroll 1
+                for (int i = lane; i < C::kQPieces; i += 32) {
+                    const uint4 next = i + 32 < C::kQPieces ? dec8_query_load<C, PAIR, RT>(args, it, i + 32) : raw;
+                    dec8_query_put<C, BF16, PAIR, RT>(args, raw, i, sQ + qb * C::NQ * 128, qf + (nq & 1) * RT);
+                    raw = next;
                 }
-                if (c == 0) qf[(nq & 1) * RT + r] = args.scale_log2 * exp2_int(e);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[qb]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[qb]);
             ++nq;
         }
     } else {
@@ -639,6 +649,12 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         const int my_r = first + (lane < RW ? lane : 0);
         const int my_hd = PAIR ? my_r / RH : 0, my_rr = PAIR ? my_r % RH : my_r;
         float* sums = reinterpret_cast<float*>(smem + C::kSumOff) + wg * 4 * RW;  // [4][RW], once per segment
+        Dec8Item first_item = rg.first;  // the one of the CTA's first segment
+        {
+            int j0, n;
+            while (first_item.P < rg.hi && !dec8_segment(rg, first_item, j0, n))
+                first_item = dec8_next(args, first_item, rg.T);
+        }
         int gk = 0, nq = 0;
         bool ok = true;
         auto meet = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
@@ -646,6 +662,16 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             if (lane == 0) mbar_arrive(bar);
             return warp_all(mbar_wait(bar, parity, wc, site));
         };
+        // The first segment's queries, a piece a thread (one warp taking them piece after piece
+        // would keep the first product waiting).
+        {
+            const int i = wg * 128 + l_idx;
+            if (i < C::kQPieces)
+                dec8_query_put<C, BF16, PAIR, RT>(args, dec8_query_load<C, PAIR, RT>(args, first_item, i), i, sQ, qf);
+            fence_proxy_async_smem();
+            named_bar_sync(1, 128 * NW);
+            if (wg == 0 && l_idx == 0) mbar_arrive(&q_full[0]);
+        }
         auto rows4 = [](const float* p, int r) { return *reinterpret_cast<const float4*>(p + r); };
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
             int j0, n;
@@ -829,30 +855,46 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             ok = drain(gk + n - 1);
             if (!ok) break;
             // Row sums over the 128 keys' threads (written again a segment later, after
-            // every warp has met at a tile in between).
+            // every warp has met at a tile in between). Each step of the sum over the warp
+            // halves the rows a lane keeps; lane RW-group g ends with row g.
 #pragma unroll
-            for (int r = 0; r < RW; ++r) {
-                float a = l[r];
+            for (int off = 16, m = RW; off > 0; off >>= 1) {
+                if (m > 1) {
+                    m >>= 1;
+                    const bool up = (lane & off) != 0;
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-                if (lane == 0) sums[w4 * RW + r] = a;
+                    for (int r = 0; r < m; ++r) {
+                        const float keep = up ? l[r + m] : l[r], give = up ? l[r] : l[r + m];
+                        l[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                    }
+                } else {
+                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
+                }
             }
-            if (lane < RW) row_m[lane] = m_run;
+            if (lane % (32 / RW) == 0) sums[w4 * RW + lane / (32 / RW)] = l[0];
             ok = meet(&meets[2], nq & 1, 134);
             if (!ok) break;
             const size_t slot = static_cast<size_t>(cta) + static_cast<size_t>(it.b) * args.HV + it.vh;
+            const int rows = min(args.RC, args.R - ch * args.RC);  // of each head
+            auto valid = [&](int rt) {
+                return (PAIR ? rt % RH : rt) < rows && (PAIR ? 2 * hh + rt / RH : hh) < args.Hkv;
+            };
+            if (lane < RW) {
+                const float lt = sums[lane] + sums[RW + lane] + sums[2 * RW + lane] + sums[3 * RW + lane];
+                row_a[lane] = lt == 0.f ? 0.f : 1.f / lt;  // no key: 0; NaN stays NaN
+                if (w4 == 0 && valid(my_r))
+                    args.lse_part[slot * RT + my_r] = lt == 0.f ? -INFINITY : m_run + log2f(lt);
+            }
+            __syncwarp();
+            float* op = args.o_part + (slot * RT + first) * D + (PAIR ? l_idx & 63 : l_idx);
 #pragma unroll
-            for (int r = 0; r < RW; ++r) {
-                const int rt = first + r;
-                const int hd = PAIR ? rt / RH : 0, rr = PAIR ? rt % RH : rt;
-                const int head = PAIR ? 2 * hh + hd : hh;
-                if (rr < args.RC && ch * args.RC + rr < args.R && head < args.Hkv) {
-                    const float lt = sums[r] + sums[RW + r] + sums[2 * RW + r] + sums[3 * RW + r];
-                    // no key: 0; NaN stays NaN
-                    const float v = lt == 0.f ? 0.f : __fdividef(acc[r], lt);
-                    if (!PAIR || (l_idx >> 6) == hd) args.o_part[(slot * RT + rt) * D + (PAIR ? l_idx & 63 : l_idx)] = v;
-                    if (l_idx == r) args.lse_part[slot * RT + rt] = lt == 0.f ? -INFINITY : row_m[r] + log2f(lt);
-                }
+            for (int r = 0; r < RW; r += 4) {
+                const float4 f4 = rows4(row_a, r);
+                const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (valid(first + r + i) && (!PAIR || (l_idx >> 6) == (first + r + i) / RH))
+                        op[(r + i) * D] = acc[r + i] * f[i];
             }
             gk += n;
             ++nq;
