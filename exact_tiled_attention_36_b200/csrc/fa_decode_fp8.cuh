@@ -24,10 +24,15 @@
 // frees the accumulation from rescaling in TMEM, and block factors of V of any size
 // enter f (the tile's largest) and P (a block's share of it).
 //
-// Work split, segments and merge: as fa_decode.cuh (stream-K over the key tiles of all
-// items laid end to end). An item is (sequence, KV head, chunk of RC query rows). d = 64:
-// an item takes two adjacent KV heads, whose code rows form one 128-byte row; S^T of each
-// is a product over its own 64 bytes, O^T lanes 64 k .. hold head k.
+// Work split: an item is (sequence, KV head, chunk of RC query rows); d = 64: two adjacent
+// KV heads, whose code rows form one 128-byte row (S^T of each is a product over its own 64
+// bytes, O^T lanes 64 k .. hold head k). TS neighbouring items of a sequence form a group
+// and are walked in step by a team of TS CTAs, one item each: a token's codes of all heads
+// lie together, and 128 bytes of each 1 KB at a time, by CTAs at different places, cost
+// DRAM its page hits (8192 keys x 8 heads x 32 sequences: 100 us; in step 86 us). Chunks of
+// one head in a team meet in the L2. The groups' key tiles, laid end to end, are split
+// evenly over the teams (stream-K) as fa_decode.cuh splits items over CTAs, with the same
+// segments and merge.
 //
 // Two CTAs share an SM, so one's softmax overlaps the other's products and loads. Warp
 // roles: warp 0 TMA producer (its lanes issue the boxes of a tile), warp 1 TMEM and the
@@ -50,20 +55,21 @@ struct Decode8Args {
     float* lse;              // [B, Hq, Nq]
     float* o_part;           // [slots, RT, d] normalised partial outputs
     float* lse_part;         // [slots, RT], log2
-    int2* meta;              // [items]: the CTAs that hold an item's first and last tile
+    int2* meta;              // [items]: the teams that hold an item's first and last tile
     const int* seqlens;      // [B] or null (every sequence has cap keys)
     const int* block_table;  // [B, per_seq]; null: contiguous
     int B, Hq, Hkv, group, Nq, R;
     int cap, per_seq, num_pages;       // keys a sequence can hold, its blocks, pages of the pool
     int page_size, page_box;           // rows of a page and of one TMA box (contiguous: 128)
     int HV, nch, RC;         // items of a sequence = heads (or pairs) x chunks of RC rows
-    int G;                   // CTAs of the split kernel
+    int TS, HG;              // items of a group, groups of a sequence (HV = TS HG)
+    int teams;               // CTAs of the split kernel: teams x TS
     float scale_log2;
     int* err;
 };
 
 constexpr int kDec8Ctas = 2;       // per SM
-constexpr int kDec8ItemCost = 2;   // units of a segment's fixed work (see kDecItemCost)
+constexpr int kDec8ItemCost = 1;   // units of a segment's fixed work (see kDecItemCost)
 
 template <bool BF16, bool PAIR, int RT>
 struct Dec8Cfg {
@@ -106,7 +112,7 @@ struct Dec8Cfg {
 // ------------------------------------------------------------------- work split
 struct Dec8Item {
     int b, vh, len, ntk, cost;
-    long long P;  // first unit of its cost
+    long long P;  // first unit of its group's cost
 };
 
 __device__ __forceinline__ int dec8_len(const Decode8Args& a, int b) {
@@ -124,10 +130,10 @@ __device__ __forceinline__ Dec8Item dec8_item(const Decode8Args& a, int b, int v
     return it;
 }
 
-// The item after `it`; past the last one P = T.
+// This CTA's item of the group after that of `it`; past the last one P = T.
 __device__ __forceinline__ Dec8Item dec8_next(const Decode8Args& a, const Dec8Item& it, long long T) {
-    if (it.vh + 1 < a.HV) return dec8_item(a, it.b, it.vh + 1, it.len, it.P + it.cost);
-    if (it.b + 1 < a.B) return dec8_item(a, it.b + 1, 0, dec8_len(a, it.b + 1), it.P + it.cost);
+    if (it.vh + a.TS < a.HV) return dec8_item(a, it.b, it.vh + a.TS, it.len, it.P + it.cost);
+    if (it.b + 1 < a.B) return dec8_item(a, it.b + 1, it.vh % a.TS, dec8_len(a, it.b + 1), it.P + it.cost);
     Dec8Item e = it;
     e.P = T;
     e.ntk = e.cost = 0;
@@ -149,6 +155,12 @@ struct Dec8Range {
     Dec8Item first;
 };
 
+// Slot of team c's segment of item vh of sequence b (the team's segments are of ascending
+// groups, and its last group is at most the next team's first: team + group is unique).
+__device__ __forceinline__ size_t dec8_slot(const Decode8Args& a, int team, int b, int vh) {
+    return (static_cast<size_t>(team) + static_cast<size_t>(b) * a.HG + vh / a.TS) * a.TS + vh % a.TS;
+}
+
 // The key tiles [j0, j0 + n) of an item in the CTA's range (false: none).
 __device__ __forceinline__ bool dec8_segment(const Dec8Range& rg, const Dec8Item& it, int& j0, int& n) {
     const long long r0 = it.P + kDec8ItemCost;
@@ -159,19 +171,19 @@ __device__ __forceinline__ bool dec8_segment(const Dec8Range& rg, const Dec8Item
     return true;
 }
 
-// The CTA's range of the T units and the item that holds its first one; called by every
-// thread (it synchronises the CTA). False, for every thread, when the CTA has none: only
-// min(G, T) CTAs share the units, so each of those has one at least. Uses misc + 8 .. 223.
+// The team's range of the T units and the item of the group that holds its first one;
+// called by every thread (it synchronises the CTA). False, for every thread, when the team
+// has none: only min(teams, T) share the units, so each of those has one at least. Uses misc + 8 .. 223.
 template <int THREADS>
 __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc, Dec8Range& rg) {
-    const int cta = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
-    const int warp = warp_id(), lane = lane_id();
+    const int team = static_cast<int>(blockIdx.x) / a.TS, hl = static_cast<int>(blockIdx.x) % a.TS;
+    const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = lane_id();
     constexpr int kWarps = THREADS / 32;
     auto range = [&] {
-        const int G = static_cast<int>(min(static_cast<long long>(a.G), rg.T));
-        if (cta >= G) return false;
-        rg.lo = dec8_muldiv(cta, rg.T, G);
-        rg.hi = dec8_muldiv(cta + 1, rg.T, G);
+        const int n = static_cast<int>(min(static_cast<long long>(a.teams), rg.T));
+        if (team >= n) return false;
+        rg.lo = dec8_muldiv(team, rg.T, n);
+        rg.hi = dec8_muldiv(team + 1, rg.T, n);
         return true;
     };
     int b0;
@@ -185,7 +197,7 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
         auto units_of = [&](int b) -> long long {
             if (b >= a.B) return 0;
             const int ntk = (dec8_len(a, b) + 127) / 128;
-            return ntk > 0 ? static_cast<long long>(a.HV) * (ntk + kDec8ItemCost) : 0;
+            return ntk > 0 ? static_cast<long long>(a.HG) * (ntk + kDec8ItemCost) : 0;
         };
         // The first THREADS sequences are scanned while the others are only summed; a CTA whose
         // range starts further on scans on from there.
@@ -234,7 +246,7 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
         P0 = *sh_P0;
     } else {
         const int ntk = (a.cap + 127) / 128;
-        const long long per_b = ntk > 0 ? static_cast<long long>(a.HV) * (ntk + kDec8ItemCost) : 0;
+        const long long per_b = ntk > 0 ? static_cast<long long>(a.HG) * (ntk + kDec8ItemCost) : 0;
         rg.T = per_b * a.B;
         if (!range()) return false;
         b0 = dec8_div(rg.lo, per_b);
@@ -242,8 +254,8 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
     }
     const int len = dec8_len(a, b0);
     const int cost = (len + 127) / 128 + kDec8ItemCost;
-    const int vh = dec8_div(rg.lo - P0, cost);
-    rg.first = dec8_item(a, b0, vh, len, P0 + static_cast<long long>(vh) * cost);
+    const int hg = dec8_div(rg.lo - P0, cost);
+    rg.first = dec8_item(a, b0, hg * a.TS + hl, len, P0 + static_cast<long long>(hg) * cost);
     return true;
 }
 
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     constexpr int D = PAIR ? 64 : 128;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (!smem_base_ok(smem, args.err)) return;
-    const int cta = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
+    const int team = static_cast<int>(blockIdx.x) / args.TS, tid = static_cast<int>(threadIdx.x);
     const int warp = warp_id(), lane = lane_id();
     uint8_t* misc = smem + C::kMiscOff;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
@@ -463,8 +475,8 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             if (!dec8_segment(rg, it, j0, n)) continue;
             if (lane == 0) {
                 int2* m = args.meta + static_cast<size_t>(it.b) * args.HV + it.vh;
-                if (j0 == 0) m->x = cta;
-                if (j0 + n == it.ntk) m->y = cta;
+                if (j0 == 0) m->x = team;
+                if (j0 + n == it.ntk) m->y = team;
             }
             const int x0 = (it.vh / args.nch) * 128;  // the head's (or pair's) first byte of a row
             const int* bt = PAGED ? args.block_table + static_cast<size_t>(it.b) * args.per_seq : nullptr;
@@ -874,7 +886,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             if (lane % (32 / RW) == 0) sums[w4 * RW + lane / (32 / RW)] = l[0];
             ok = meet(&meets[2], nq & 1, 134);
             if (!ok) break;
-            const size_t slot = static_cast<size_t>(cta) + static_cast<size_t>(it.b) * args.HV + it.vh;
+            const size_t slot = dec8_slot(args, team, it.b, it.vh);
             const int rows = min(args.RC, args.R - ch * args.RC);  // of each head
             auto valid = [&](int rt) {
                 return (PAIR ? rt % RH : rt) < rows && (PAIR ? 2 * hh + rt / RH : hh) < args.Hkv;
@@ -929,12 +941,14 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
     const int2 cc = a.meta[item];  // of an item without keys: anything
     const int len = dec8_len(a, b);
     const int c0 = cc.x, c1 = len > 0 ? cc.y : cc.x - 1;
-    const float* lp = a.lse_part + item * RT + r;  // segment of CTA c: lp[c * RT]
-    const float4* op = reinterpret_cast<const float4*>(a.o_part + (item * RT + r) * D) + lane;
+    const size_t s0 = dec8_slot(a, 0, b, vh) * RT + r;  // the segment of team c lies c TS RT rows further
+    const size_t step = static_cast<size_t>(a.TS) * RT;
+    const float* lp = a.lse_part + s0;
+    const float4* op = reinterpret_cast<const float4*>(a.o_part + s0 * D) + lane;
     float Lm = -INFINITY;
     bool nan = false;
     for (int c = c0 + lane; c <= c1; c += 32) {
-        const float L = lp[static_cast<size_t>(c) * RT];
+        const float L = lp[c * step];
         Lm = fmaxf(Lm, L);
         nan |= L != L;
     }
@@ -942,15 +956,15 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
     nan = __any_sync(0xffffffffu, nan);
     const float ref = Lm == -INFINITY ? 0.f : Lm;
     float wsum = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) wsum += ex2_approx(lp[static_cast<size_t>(c) * RT] - ref);
+    for (int c = c0 + lane; c <= c1; c += 32) wsum += ex2_approx(lp[c * step] - ref);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (lane < D / 4) {
 #pragma unroll 4
         for (int c = c0 + warp; c <= c1; c += W) {
-            const float w = ex2_approx(lp[static_cast<size_t>(c) * RT] - ref);
-            const float4 x = op[static_cast<size_t>(c) * (RT * D / 4)];
+            const float w = ex2_approx(lp[c * step] - ref);
+            const float4 x = op[c * step * (D / 4)];
             acc.x = fmaf(w, x.x, acc.x);
             acc.y = fmaf(w, x.y, acc.y);
             acc.z = fmaf(w, x.z, acc.z);

@@ -106,13 +106,13 @@ fa_status append8(const void* k, const void* v, const long long* k_strides, cons
     return d == 64 ? launch_append8<false, 64>(a, chunks, s) : launch_append8<false, 128>(a, chunks, s);
 }
 
-// How a call's rows become items, and its workspace: meta (each item's first and last CTA), the
-// partial L and O (fp32) of slots = CTAs + items, RT rows each.
+// How a call's rows become items, and its workspace: meta (each item's first and last team), the
+// partial L and O (fp32) of slots = teams x TS + items, RT rows each.
 struct Dec8Plan {
     int rt;       // rows of a tile: the smallest of 4, 8, 16 that holds a head's (d = 64: two heads') rows
     int nch, RC;  // chunks a head's rows are cut into, and rows of a chunk
-    int HV;
-    long long items, ctas;
+    int HV, TS;   // items of a sequence, items of a group (a team of CTAs)
+    long long items, teams;
     size_t meta, lse, total;
 };
 
@@ -126,8 +126,13 @@ bool dec8_plan(int B, int Hq, int Hkv, int Nq, int d, Dec8Plan& p) {
     p.RC = (R + p.nch - 1) / p.nch;
     p.HV = (Hkv + heads - 1) / heads * p.nch;
     p.items = static_cast<long long>(B) * p.HV;
-    p.ctas = static_cast<long long>(sms) * fa::kDec8Ctas;
-    const size_t slots = static_cast<size_t>(p.items + p.ctas) * p.rt;
+    // A team walks 8 items in step, or as many as divide a sequence's items evenly: 8 heads' codes
+    // are 1 KB of a token, and 296 CTAs make 37 teams of 8.
+    p.TS = 1;
+    for (int n = 2; n <= 16 && n <= p.HV; ++n)
+        if (p.HV % n == 0 && (n <= 8 || p.TS == 1)) p.TS = n;
+    p.teams = static_cast<long long>(sms) * fa::kDec8Ctas / p.TS;
+    const size_t slots = static_cast<size_t>(p.items + p.teams * p.TS) * p.rt;
     auto round = [](size_t x) { return (x + 255) & ~size_t(255); };
     p.meta = round(p.items * sizeof(int2));
     p.lse = round(slots * sizeof(float));
@@ -167,14 +172,14 @@ fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::
         constexpr auto kern = fa::fa_decode8_kernel<BF16, D == 64, PAGED, RT>;
         using C = fa::Dec8Cfg<BF16, D == 64, RT>;
         if (!kernel_ready<kern>(C::kSmemBytes)) return FA_ERR_CUDA;
-        cfg.gridDim = dim3(a.G);
+        cfg.gridDim = dim3(a.teams * a.TS);
         cfg.blockDim = dim3(C::kThreads);
         cfg.dynamicSmemBytes = C::kSmemBytes;
         if (cudaLaunchKernelEx(&cfg, kern, mk, mv, a, causal) != cudaSuccess) return FA_ERR_CUDA;
     }
-    // A row's segments: about CTAs / items, one or two more where ranges cross.
+    // A row's segments: about teams / groups, one or two more where ranges cross.
     const int rows = a.B * a.Hq * a.Nq;
-    const bool wide = a.G > 6LL * a.B * a.HV;
+    const bool wide = a.teams > 6LL * a.B * a.HG;
     cfg.gridDim = dim3(wide ? rows : (rows + 3) / 4);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
@@ -269,7 +274,10 @@ fa_status decode8(const void* q, const void* k, const void* v, const float* k_sc
     a.HV = pl.HV;
     a.nch = pl.nch;
     a.RC = pl.RC;
-    a.G = static_cast<int>(tiles < pl.ctas ? (tiles > 0 ? tiles : 1) : pl.ctas);
+    a.TS = pl.TS;
+    a.HG = pl.HV / pl.TS;
+    const long long group_tiles = tiles / pl.TS;
+    a.teams = static_cast<int>(group_tiles < pl.teams ? (group_tiles > 0 ? group_tiles : 1) : pl.teams);
     a.scale_log2 = scale * kLog2e;
     const cudaStream_t s = cu(stream);
     if (dtype == FA_BF16) return launch_dec8<true>(pl.rt, d, paged, mk, mv, a, causal, tiles > 0, s);
