@@ -99,7 +99,8 @@ struct Dec8Cfg {
     static constexpr int kRedOff = kQfOff + 2 * RT * 4;           // float [NW][2][4][RW]: warps' maxima
     static constexpr int kRowOff = kRedOff + 8 * RT * 4;          // float [NW][4][5][RW]: a warp's row values
     static constexpr int kSumOff = kRowOff + 20 * RT * 4;         // float [NW][4][RW]: warps' sums
-    static constexpr int kSmemBytes = kSumOff + 4 * RT * 4;
+    static constexpr int kLenOff = kSumOff + 4 * RT * 4;          // int [kThreads]: lengths of the first sequences
+    static constexpr int kSmemBytes = kLenOff + kThreads * 4;
     static constexpr uint32_t kColO = 2 * NQ;                     // S^T buffers at 0 and NQ
     static constexpr uint32_t kCols = 2 * NQ + 2 * N;
     static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
@@ -110,8 +111,10 @@ struct Dec8Cfg {
 };
 
 // ------------------------------------------------------------------- work split
+// One CTA's item: group hg of sequence b, and in it the CTA's place hl of the team, which
+// is item vh = hg TS + hl: chunk ch of the rows of KV head (d = 64: pair of heads) hh.
 struct Dec8Item {
-    int b, vh, len, ntk, cost;
+    int b, hg, hh, ch, len, ntk, cost;
     long long P;  // first unit of its group's cost
 };
 
@@ -119,25 +122,22 @@ __device__ __forceinline__ int dec8_len(const Decode8Args& a, int b) {
     return a.seqlens ? min(max(a.seqlens[b], 0), a.cap) : a.cap;
 }
 
-__device__ __forceinline__ Dec8Item dec8_item(const Decode8Args& a, int b, int vh, int len, long long P) {
+__device__ __forceinline__ Dec8Item dec8_item(const Decode8Args& a, int b, int hg, int hl, int len, long long P) {
     Dec8Item it;
     it.b = b;
-    it.vh = vh;
+    it.hg = hg;
+    const int vh = hg * a.TS + hl;
+    it.hh = vh;
+    it.ch = 0;
+    if (a.nch > 1) {  // (a division costs as much as a small tile's softmax row)
+        it.hh = vh / a.nch;
+        it.ch = vh - it.hh * a.nch;
+    }
     it.len = len;
     it.ntk = (len + 127) / 128;
     it.cost = it.ntk > 0 ? it.ntk + kDec8ItemCost : 0;
     it.P = P;
     return it;
-}
-
-// This CTA's item of the group after that of `it`; past the last one P = T.
-__device__ __forceinline__ Dec8Item dec8_next(const Decode8Args& a, const Dec8Item& it, long long T) {
-    if (it.vh + a.TS < a.HV) return dec8_item(a, it.b, it.vh + a.TS, it.len, it.P + it.cost);
-    if (it.b + 1 < a.B) return dec8_item(a, it.b + 1, it.vh % a.TS, dec8_len(a, it.b + 1), it.P + it.cost);
-    Dec8Item e = it;
-    e.P = T;
-    e.ntk = e.cost = 0;
-    return e;
 }
 
 // a b / c and a / b, in 32 bits where the operands allow it (64-bit divisions are calls).
@@ -152,13 +152,30 @@ __device__ __forceinline__ int dec8_div(long long a, long long b) {
 
 struct Dec8Range {
     long long T, lo, hi;
+    int team, hl;
+    const int* lens;  // shared memory: the first n_lens sequences' lengths (a load from global memory
+    int n_lens;       // takes a microsecond or more while the caches stream)
     Dec8Item first;
 };
 
-// Slot of team c's segment of item vh of sequence b (the team's segments are of ascending
-// groups, and its last group is at most the next team's first: team + group is unique).
-__device__ __forceinline__ size_t dec8_slot(const Decode8Args& a, int team, int b, int vh) {
-    return (static_cast<size_t>(team) + static_cast<size_t>(b) * a.HG + vh / a.TS) * a.TS + vh % a.TS;
+// This CTA's item of the group after that of `it`; past the last one P = T.
+__device__ __forceinline__ Dec8Item dec8_next(const Decode8Args& a, const Dec8Range& rg, const Dec8Item& it) {
+    if (it.hg + 1 < a.HG) return dec8_item(a, it.b, it.hg + 1, rg.hl, it.len, it.P + it.cost);
+    if (it.b + 1 < a.B) {
+        const int len = it.b + 1 < rg.n_lens ? rg.lens[it.b + 1] : dec8_len(a, it.b + 1);
+        return dec8_item(a, it.b + 1, 0, rg.hl, len, it.P + it.cost);
+    }
+    Dec8Item e = it;
+    e.P = rg.T;
+    e.ntk = e.cost = 0;
+    return e;
+}
+
+// Slot of a team's segment of item (hg, hl) of sequence b (the team's segments are of
+// ascending groups, and its last group is at most the next team's first: team + group is
+// unique).
+__device__ __forceinline__ size_t dec8_slot(const Decode8Args& a, int team, int b, int hg, int hl) {
+    return (static_cast<size_t>(team) + static_cast<size_t>(b) * a.HG + hg) * a.TS + hl;
 }
 
 // The key tiles [j0, j0 + n) of an item in the CTA's range (false: none).
@@ -175,19 +192,22 @@ __device__ __forceinline__ bool dec8_segment(const Dec8Range& rg, const Dec8Item
 // called by every thread (it synchronises the CTA). False, for every thread, when the team
 // has none: only min(teams, T) share the units, so each of those has one at least. Uses misc + 8 .. 223.
 template <int THREADS>
-__device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc, Dec8Range& rg) {
-    const int team = static_cast<int>(blockIdx.x) / a.TS, hl = static_cast<int>(blockIdx.x) % a.TS;
+__device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc, int* lens, Dec8Range& rg) {
     const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = lane_id();
+    rg.team = static_cast<int>(blockIdx.x) / a.TS;
+    rg.hl = static_cast<int>(blockIdx.x) - rg.team * a.TS;
     constexpr int kWarps = THREADS / 32;
     auto range = [&] {
         const int n = static_cast<int>(min(static_cast<long long>(a.teams), rg.T));
-        if (team >= n) return false;
-        rg.lo = dec8_muldiv(team, rg.T, n);
-        rg.hi = dec8_muldiv(team + 1, rg.T, n);
+        if (rg.team >= n) return false;
+        rg.lo = dec8_muldiv(rg.team, rg.T, n);
+        rg.hi = dec8_muldiv(rg.team + 1, rg.T, n);
         return true;
     };
     int b0;
     long long P0;
+    rg.lens = lens;
+    rg.n_lens = 0;
     if (a.seqlens) {
         int* found = reinterpret_cast<int*>(misc + 8);
         int* sh_b0 = reinterpret_cast<int*>(misc + 12);
@@ -196,11 +216,14 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
         long long* wr = ws + kWarps;                              // sums of the rest
         auto units_of = [&](int b) -> long long {
             if (b >= a.B) return 0;
-            const int ntk = (dec8_len(a, b) + 127) / 128;
+            const int len = dec8_len(a, b);
+            if (b < THREADS) lens[b] = len;
+            const int ntk = (len + 127) / 128;
             return ntk > 0 ? static_cast<long long>(a.HG) * (ntk + kDec8ItemCost) : 0;
         };
         // The first THREADS sequences are scanned while the others are only summed; a CTA whose
         // range starts further on scans on from there.
+        rg.n_lens = min(a.B, THREADS);
         long long x = units_of(tid), rest = 0;
         for (int b = tid + THREADS; b < a.B; b += THREADS) rest += units_of(b);
         long long incl = x, run = 0;
@@ -252,10 +275,10 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
         b0 = dec8_div(rg.lo, per_b);
         P0 = b0 * per_b;
     }
-    const int len = dec8_len(a, b0);
+    const int len = b0 < rg.n_lens ? lens[b0] : dec8_len(a, b0);
     const int cost = (len + 127) / 128 + kDec8ItemCost;
     const int hg = dec8_div(rg.lo - P0, cost);
-    rg.first = dec8_item(a, b0, hg * a.TS + hl, len, P0 + static_cast<long long>(hg) * cost);
+    rg.first = dec8_item(a, b0, hg, rg.hl, len, P0 + static_cast<long long>(hg) * cost);
     return true;
 }
 
@@ -335,9 +358,8 @@ __device__ __forceinline__ void e4m3_terms(uint32_t x, uint32_t (&c)[NT]) {
 template <typename C, bool PAIR, int RT>
 __device__ __forceinline__ uint4 dec8_query_load(const Decode8Args& a, const Dec8Item& it, int i) {
     const int r = i / C::kRowPieces, c = i % C::kRowPieces;
-    const int hh = it.vh / a.nch, ch = it.vh % a.nch;
     const int hd = PAIR ? r / C::RH : 0, rr = PAIR ? r % C::RH : r;
-    const int gr = ch * a.RC + rr, head = PAIR ? 2 * hh + hd : hh;
+    const int gr = it.ch * a.RC + rr, head = PAIR ? 2 * it.hh + hd : it.hh;
     if (rr >= a.RC || gr >= a.R || head >= a.Hkv) return make_uint4(0, 0, 0, 0);
     const size_t row = (static_cast<size_t>(it.b) * a.Nq + gr / a.group) * a.Hq + static_cast<size_t>(head) * a.group +
                        gr % a.group;
@@ -383,8 +405,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     constexpr int D = PAIR ? 64 : 128;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (!smem_base_ok(smem, args.err)) return;
-    const int team = static_cast<int>(blockIdx.x) / args.TS, tid = static_cast<int>(threadIdx.x);
-    const int warp = warp_id(), lane = lane_id();
+    const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = lane_id();
     uint8_t* misc = smem + C::kMiscOff;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
     int* abort_flag = reinterpret_cast<int*>(misc + 4);
@@ -451,7 +472,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         tmem_relinquish();
     }
     Dec8Range rg;
-    const bool work = dec8_locate<THREADS>(args, misc, rg);
+    const bool work = dec8_locate<THREADS>(args, misc, reinterpret_cast<int*>(smem + C::kLenOff), rg);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -470,15 +491,15 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         const int pb = args.page_box;
         int u = 0;
         bool ok = true;
-        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
             if (lane == 0) {
-                int2* m = args.meta + static_cast<size_t>(it.b) * args.HV + it.vh;
-                if (j0 == 0) m->x = team;
-                if (j0 + n == it.ntk) m->y = team;
+                int2* m = args.meta + (static_cast<size_t>(it.b) * args.HG + it.hg) * args.TS + rg.hl;
+                if (j0 == 0) m->x = rg.team;
+                if (j0 + n == it.ntk) m->y = rg.team;
             }
-            const int x0 = (it.vh / args.nch) * 128;  // the head's (or pair's) first byte of a row
+            const int x0 = it.hh * 128;  // the head's (or pair's) first byte of a row
             const int* bt = PAGED ? args.block_table + static_cast<size_t>(it.b) * args.per_seq : nullptr;
             auto page_of = [&](int kt) {
                 const int key = kt * 128 + lane * pb;
@@ -529,7 +550,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             };
             int gk = 0, nq = 0;
             bool ok = true;
-            for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+            for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
                 int j0, n;
                 if (!dec8_segment(rg, it, j0, n)) continue;
                 const int qb = nq % QB;
@@ -585,11 +606,10 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         const int pb = args.page_box;
         int gk = 0;
         bool ok = true;
-        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
-            const int hh = it.vh / args.nch;
-            const int head = PAIR ? 2 * hh + h : hh;
+            const int head = PAIR ? 2 * it.hh + h : it.hh;
             const bool mine = (PAIR || h == 0) && head < args.Hkv;
             const float* f = kv ? args.v_scale : args.k_scale;
             auto read = [&](int kt) -> float {
@@ -623,7 +643,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         // ------------------------------------------------------------ query terms
         int nq = 0;
         bool ok = true;
-        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
             const int qb = nq % QB;
@@ -665,7 +685,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         {
             int j0, n;
             while (first_item.P < rg.hi && !dec8_segment(rg, first_item, j0, n))
-                first_item = dec8_next(args, first_item, rg.T);
+                first_item = dec8_next(args, rg, first_item);
         }
         int gk = 0, nq = 0;
         bool ok = true;
@@ -685,13 +705,15 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             if (wg == 0 && l_idx == 0) mbar_arrive(&q_full[0]);
         }
         auto rows4 = [](const float* p, int r) { return *reinterpret_cast<const float4*>(p + r); };
-        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, it, rg.T)) {
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
-            const int hh = it.vh / args.nch, ch = it.vh % args.nch;
-            const int my_gr = ch * args.RC + my_rr;  // this lane's row in its head's group
+            const int my_gr = it.ch * args.RC + my_rr;  // this lane's row in its head's group
             __syncwarp();
-            if (lane < RW) row_hi[lane] = causal ? min(it.len, my_gr / args.group + it.len - args.Nq + 1) : it.len;
+            if (lane < RW) {
+                const int t = causal && args.Nq > 1 ? my_gr / args.group : 0;
+                row_hi[lane] = causal ? min(it.len, t + it.len - args.Nq + 1) : it.len;
+            }
             __syncwarp();
             const int all_hi = causal ? it.len - args.Nq + 1 : it.len;  // keys below it are seen by every row
             ok = warp_all(mbar_wait(&q_full[nq % QB], (nq / QB) & 1, wc, 128));
@@ -886,16 +908,17 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             if (lane % (32 / RW) == 0) sums[w4 * RW + lane / (32 / RW)] = l[0];
             ok = meet(&meets[2], nq & 1, 134);
             if (!ok) break;
-            const size_t slot = dec8_slot(args, team, it.b, it.vh);
-            const int rows = min(args.RC, args.R - ch * args.RC);  // of each head
+            const size_t slot = dec8_slot(args, rg.team, it.b, it.hg, rg.hl);
+            const int rows = min(args.RC, args.R - it.ch * args.RC);  // of each head
             auto valid = [&](int rt) {
-                return (PAIR ? rt % RH : rt) < rows && (PAIR ? 2 * hh + rt / RH : hh) < args.Hkv;
+                return (PAIR ? rt % RH : rt) < rows && (PAIR ? 2 * it.hh + rt / RH : it.hh) < args.Hkv;
             };
             if (lane < RW) {
                 const float lt = sums[lane] + sums[RW + lane] + sums[2 * RW + lane] + sums[3 * RW + lane];
-                row_a[lane] = lt == 0.f ? 0.f : 1.f / lt;  // no key: 0; NaN stays NaN
-                if (w4 == 0 && valid(my_r))
-                    args.lse_part[slot * RT + my_r] = lt == 0.f ? -INFINITY : m_run + log2f(lt);
+                row_a[lane] = lt == 0.f ? 0.f : __fdividef(1.f, lt);  // no key: 0; NaN stays NaN
+                float lg;
+                asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(lt));
+                if (w4 == 0 && valid(my_r)) args.lse_part[slot * RT + my_r] = lt == 0.f ? -INFINITY : m_run + lg;
             }
             __syncwarp();
             float* op = args.o_part + (slot * RT + first) * D + (PAIR ? l_idx & 63 : l_idx);
@@ -941,36 +964,59 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
     const int2 cc = a.meta[item];  // of an item without keys: anything
     const int len = dec8_len(a, b);
     const int c0 = cc.x, c1 = len > 0 ? cc.y : cc.x - 1;
-    const size_t s0 = dec8_slot(a, 0, b, vh) * RT + r;  // the segment of team c lies c TS RT rows further
+    const size_t s0 = dec8_slot(a, 0, b, vh / a.TS, vh % a.TS) * RT + r;  // the segment of team c lies c TS RT rows further
     const size_t step = static_cast<size_t>(a.TS) * RT;
     const float* lp = a.lse_part + s0;
     const float4* op = reinterpret_cast<const float4*>(a.o_part + s0 * D) + lane;
-    float Lm = -INFINITY;
+    float Lm = -INFINITY, wsum = 0.f;
     bool nan = false;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-        const float L = lp[c * step];
-        Lm = fmaxf(Lm, L);
-        nan |= L != L;
-    }
-    Lm = warp_max(Lm);
-    nan = __any_sync(0xffffffffu, nan);
-    const float ref = Lm == -INFINITY ? 0.f : Lm;
-    float wsum = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) wsum += ex2_approx(lp[c * step] - ref);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (lane < D / 4) {
-#pragma unroll 4
-        for (int c = c0 + warp; c <= c1; c += W) {
-            const float w = ex2_approx(lp[c * step] - ref);
-            const float4 x = op[c * step * (D / 4)];
-            acc.x = fmaf(w, x.x, acc.x);
-            acc.y = fmaf(w, x.y, acc.y);
-            acc.z = fmaf(w, x.z, acc.z);
-            acc.w = fmaf(w, x.w, acc.w);
+    auto add = [&](float w, const float4& x) {
+        acc.x = fmaf(w, x.x, acc.x);
+        acc.y = fmaf(w, x.y, acc.y);
+        acc.z = fmaf(w, x.z, acc.z);
+        acc.w = fmaf(w, x.w, acc.w);
+    };
+    constexpr int kFew = 4;
+    const bool mine = lane < D / 4;
+    if (!WIDE && c1 - c0 < kFew) {
+        // Every load in flight at once, every lane with all the weights.
+        float L[kFew];
+        float4 x[kFew];
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            L[i] = c0 + i <= c1 ? lp[(c0 + i) * step] : -INFINITY;
+            x[i] = c0 + i <= c1 && mine ? op[(c0 + i) * step * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (WIDE) part[warp][lane] = acc;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            Lm = fmaxf(Lm, L[i]);
+            nan |= L[i] != L[i];
+        }
+        const float ref = Lm == -INFINITY ? 0.f : Lm;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            const float w = ex2_approx(L[i] - ref);
+            wsum += w;
+            add(w, x[i]);
+        }
+    } else {
+        for (int c = c0 + lane; c <= c1; c += 32) {
+            const float L = lp[c * step];
+            Lm = fmaxf(Lm, L);
+            nan |= L != L;
+        }
+        Lm = warp_max(Lm);
+        nan = __any_sync(0xffffffffu, nan);
+        const float ref = Lm == -INFINITY ? 0.f : Lm;
+        for (int c = c0 + lane; c <= c1; c += 32) wsum += ex2_approx(lp[c * step] - ref);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
+        if (mine) {
+#pragma unroll 4
+            for (int c = c0 + warp; c <= c1; c += W) add(ex2_approx(lp[c * step] - ref), op[c * step * (D / 4)]);
+            if (WIDE) part[warp][lane] = acc;
+        }
     }
     if constexpr (WIDE) {
         __syncthreads();
@@ -987,7 +1033,7 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
         }
     }
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    if (lane < D / 4)
+    if (mine)
         *reinterpret_cast<uint2*>(a.o + static_cast<size_t>(row) * D + lane * 4) =
             make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
     if (lane == 0)
