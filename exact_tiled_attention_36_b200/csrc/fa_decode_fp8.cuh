@@ -283,6 +283,13 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
 }
 
 // ------------------------------------------------------------------- primitives
+// Descriptor of an unswizzled K-major operand: 8-row x 16-byte pieces of 128 contiguous
+// bytes, `k` bytes apart along K and `mn` bytes apart along the rows.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t k, uint32_t mn) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((k >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((mn >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
 // N columns of this thread's TMEM lane. The values may be used after tmem_ld_done and a
 // tie (which keeps the compiler from moving their uses above it).
 template <int N>
@@ -574,7 +581,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_ss_f8(tmem + C::kColO + static_cast<uint32_t>(b * C::N), sdesc_sw128(v_addr + kk * 4096, C::kTile, 1024),
-                                  sdesc_sw128(p_addr + kk * 32, 16, 1024), id_pv, kk > 0 ? 1u : 0u);
+                                  sdesc_plain(p_addr + kk * 256, 128, 1024), id_pv, kk > 0 ? 1u : 0u);
                     tc_commit(&pv_done[b]);
                     tc_commit(&empty[uv % U]);
                     if (j + 2 < n) {  // S^T of tile gg + 2 into the buffer that p_full says was read
@@ -826,7 +833,9 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 moved = __any_sync(0xffffffffu, moved);
                 __syncwarp();
                 // P = 2^(x - m_tile), its sum in the running scale, and its terms times V's share.
-                uint8_t* pb = sP + par * C::N * 128;
+                // Row n, key l in the unswizzled layout: rows at constant offsets from the key's place
+                // (the 128-byte swizzle would cost an address of its own for every row).
+                uint8_t* pb = sP + par * C::N * 128 + (first >> 3) * 1024 + (first & 7) * 16 + (l_idx >> 4) * 128 + (l_idx & 15);
 #pragma unroll
                 for (int r = 0; r < RW; r += 4) {
                     const float4 m4 = rows4(row_m, r), f4 = rows4(row_f + par * RW, r);
@@ -848,10 +857,9 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                                                     p1 * (kMixed && r + i + 1 >= RH ? vs1 : vs0)), c);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            const int n0 = t * RT + first + r + i;
-                            pb[n0 * 128 + (((l_idx >> 4) ^ (n0 & 7)) << 4) + (l_idx & 15)] = static_cast<uint8_t>(c[t]);
-                            pb[(n0 + 1) * 128 + (((l_idx >> 4) ^ ((n0 + 1) & 7)) << 4) + (l_idx & 15)] =
-                                static_cast<uint8_t>(c[t] >> 8);
+                            const int n0 = t * RT + r + i, n1 = n0 + 1;  // past the warpgroup's first row
+                            pb[(n0 >> 3) * 1024 + (n0 & 7) * 16] = static_cast<uint8_t>(c[t]);
+                            pb[(n1 >> 3) * 1024 + (n1 & 7) * 16] = static_cast<uint8_t>(c[t] >> 8);
                         }
                     }
                 }
@@ -939,14 +947,15 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     }
 }
 
-// Merge of the segments of each output row of [B, Nq, Hq]. WIDE: one block of four warps
-// per row (warp w takes every fourth segment), for items split over many CTAs; else one
+// Merge of the segments of each output row of [B, Nq, Hq]. WIDE: one block of eight warps
+// per row (warp w takes every eighth segment), for items split over many teams; else one
 // warp per row. A lane holds four values.
+constexpr int kDec8WideWarps = 8;
 template <int D, bool BF16, int RT, bool WIDE>
-__global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, const int rows) {
+__global__ void __launch_bounds__(WIDE ? 32 * kDec8WideWarps : 128) fa_decode8_combine(const Decode8Args a, const int rows) {
     constexpr bool PAIR = D == 64;
     constexpr int RH = PAIR ? RT / 2 : RT;
-    constexpr int W = WIDE ? 4 : 1;
+    constexpr int W = WIDE ? kDec8WideWarps : 1;
     __shared__ float4 part[W][D / 4];
     const int lane = lane_id(), warp = WIDE ? warp_id() : 0;
     const int row = WIDE ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * 4 + warp_id();
@@ -963,7 +972,7 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
     asm volatile("griddepcontrol.launch_dependents;");
     const int2 cc = a.meta[item];  // of an item without keys: anything
     const int len = dec8_len(a, b);
-    const int c0 = cc.x, c1 = len > 0 ? cc.y : cc.x - 1;
+    const int c0 = len > 0 ? cc.x : 0, c1 = len > 0 ? cc.y : -1;
     const size_t s0 = dec8_slot(a, 0, b, vh / a.TS, vh % a.TS) * RT + r;  // the segment of team c lies c TS RT rows further
     const size_t step = static_cast<size_t>(a.TS) * RT;
     const float* lp = a.lse_part + s0;
@@ -977,7 +986,7 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
         acc.z = fmaf(w, x.z, acc.z);
         acc.w = fmaf(w, x.w, acc.w);
     };
-    constexpr int kFew = 4;
+    constexpr int kFew = WIDE ? 6 : 4;
     const bool mine = lane < D / 4;
     if (!WIDE && c1 - c0 < kFew) {
         // Every load in flight at once, every lane with all the weights.
@@ -1001,6 +1010,12 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
             add(w, x[i]);
         }
     } else {
+        float4 x[kFew];  // of the warp's first segments, on their way before the weights are known
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            const int c = c0 + warp + i * W;
+            x[i] = c <= c1 && mine ? op[c * step * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         for (int c = c0 + lane; c <= c1; c += 32) {
             const float L = lp[c * step];
             Lm = fmaxf(Lm, L);
@@ -1012,11 +1027,14 @@ __global__ void __launch_bounds__(128) fa_decode8_combine(const Decode8Args a, c
         for (int c = c0 + lane; c <= c1; c += 32) wsum += ex2_approx(lp[c * step] - ref);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
-        if (mine) {
-#pragma unroll 4
-            for (int c = c0 + warp; c <= c1; c += W) add(ex2_approx(lp[c * step] - ref), op[c * step * (D / 4)]);
-            if (WIDE) part[warp][lane] = acc;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            const int c = c0 + warp + i * W;
+            if (c <= c1) add(ex2_approx(lp[c * step] - ref), x[i]);
         }
+        if (mine)
+            for (int c = c0 + warp + kFew * W; c <= c1; c += W) add(ex2_approx(lp[c * step] - ref), op[c * step * (D / 4)]);
+        if (WIDE && mine) part[warp][lane] = acc;
     }
     if constexpr (WIDE) {
         __syncthreads();

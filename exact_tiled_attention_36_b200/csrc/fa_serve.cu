@@ -181,7 +181,7 @@ fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::
     const int rows = a.B * a.Hq * a.Nq;
     const bool wide = a.teams > 6LL * a.B * a.HG;
     cfg.gridDim = dim3(wide ? rows : (rows + 3) / 4);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(wide ? 32 * fa::kDec8WideWarps : 128);
     cfg.dynamicSmemBytes = 0;
     if ((wide ? cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT, true>, a, rows)
               : cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT, false>, a, rows)) != cudaSuccess)

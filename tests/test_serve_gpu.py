@@ -242,6 +242,19 @@ def test_decode_workspace_kept_between_layouts():
         check_decode(o, lse, cache.reference(q, d ** -0.5, False), q.dtype)
 
 
+@pytest.mark.parametrize("word", [-2 ** 31, 2 ** 31 - 1, 0, -1])
+def test_decode_workspace_contents_do_not_matter(word):
+    """Empty sequences among others, one of them alone, whatever the workspace holds on entry."""
+    for lens, cap in (([0, 700, 0, 1, 0], 700), ([0], 128)):
+        B = len(lens)
+        ws = torch.empty(fb.fa_decode_fp8_workspace_size(B, 8, 2, 1, 128) // 4, dtype=I32, device="cuda").fill_(word)
+        cache = Cache(B, cap, 2, 128, 0, lens, seed=23)
+        q = queries(B, 1, 8, 128, "bf16", 24)
+        k, v, kf, vf = cache.cuda()
+        o, lse = fb.attention_decode_fp8(q, k, v, kf, vf, dev(lens), workspace=ws.view(torch.uint8))
+        check_decode(o, lse, cache.reference(q, 128 ** -0.5, False), q.dtype)
+
+
 def test_decode_is_deterministic_and_takes_any_stream():
     cache = Cache(6, 3000, 2, 128, 64, [3000, 1, 2999, 128, 1500, 777], seed=20)
     q = queries(6, 1, 16, 128, "bf16", 21)
