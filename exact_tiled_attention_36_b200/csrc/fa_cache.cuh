@@ -230,11 +230,14 @@ __global__ void __launch_bounds__(256) fa_append16_kernel(const Append16Args a) 
 // rounded again. Infinities and NaN count for no factor and are stored as NaN.
 //
 // One group of TG threads takes one (block, KV head, key or value): it reads the new
-// rows once, holding them in registers (16 bytes a chunk, kHold chunks a thread) for
-// the maximum and the codes. TG is the smallest of 32, 64, 128 and 256 whose registers
-// hold the rows a block can get, so that every thread has kHold loads in flight (what
-// bounds it is their latency: 256 threads for 64-row blocks, four loads each, took 45 us
-// for 18,000 tokens of 8 heads). Groups of a warp share CTAs of eight.
+// rows once, holding them (16 bytes a chunk, kHold chunks a thread) for the maximum and
+// the codes. TG is the smallest of 32, 64, 128 and 256 whose threads hold the rows a
+// block can get, so that every thread has kHold copies in flight (18,000 tokens of 8
+// heads: 31 us; 256 threads for 64-row blocks, four loads each: 45 us). They go to shared
+// memory, each thread reading back its own. The maximum is taken of the 16-bit patterns,
+// two at a time, and the test for infinities and NaN once per group, not per value: with
+// both in fp32 the kernel was bound by issuing instructions. Groups of a warp share CTAs
+// of eight.
 struct Append8Args {
     const uint16_t* x[2];  // k, v
     uint8_t* codes[2];
@@ -279,13 +282,14 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
     }
 }
 
-// Eight values times `inv` (a power of two) as E4M3 codes; what is not finite becomes NaN.
-__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        y[i] = (__float_as_uint(f[i]) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : f[i] * inv;
-    return make_uint2(pack4_e4m3(y[0], y[1], y[2], y[3]), pack4_e4m3(y[4], y[5], y[6], y[7]));
+// The larger of two pairs of 16-bit magnitudes, with those of `u` (a pair of values);
+// `finite`: infinities and NaN count as 0.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_magnitude2(uint32_t m, uint32_t u, bool finite) {
+    constexpr uint32_t kInf2 = BF16 ? 0x7f807f80u : 0x7c007c00u;
+    u &= 0x7fff7fffu;
+    if (finite) u &= __vcmpltu2(u, kInf2);
+    return __vmaxu2(m, u);
 }
 
 // Four E4M3 codes times `ratio`, rounded to E4M3 again.
@@ -299,10 +303,11 @@ __device__ __forceinline__ uint32_t rescale4_e4m3(uint32_t c, float ratio) {
 }
 
 template <bool BF16, int D, int TG>
-__global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 4 : 1024 / TG) fa_append8_kernel(const Append8Args a) {
+__global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 5 : 1280 / TG) fa_append8_kernel(const Append8Args a) {
     constexpr int kChunks = D / 8;            // 16-byte chunks of a row
     constexpr int kRows = TG / kChunks;       // rows a group reads at a time
-    __shared__ float red[8];
+    __shared__ uint32_t red[2][8];
+    __shared__ uint4 held[kHold][TG == 32 ? 256 : TG];
     const int lane = lane_id(), warp = warp_id();
     const long long grp = TG == 32 ? static_cast<long long>(blockIdx.x) * 8 + warp : blockIdx.x;
     if (grp >= a.groups) return;  // uniform over the group
@@ -329,12 +334,17 @@ __global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 4 : 1024 / TG)
     // The rows are on their way before the block's place is looked up.
     const uint16_t* src = a.x[kv] + (t0 + p0 - old) * a.st[kv] + h * a.sh[kv];
     const int c = tg % kChunks, r_first = tg / kChunks;
-    uint4 held[kHold];
+    uint4* mine = &held[0][threadIdx.x];
+    constexpr int kStride = TG == 32 ? 256 : TG;
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
         const int r = r_first + i * kRows;
-        if (r < rows) held[i] = *reinterpret_cast<const uint4*>(src + r * a.st[kv] + c * 8);
+        if (r < rows)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(mine + i * kStride)),
+                         "l"(src + r * a.st[kv] + c * 8)
+                         : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     const int per_row = a.Hkv * D;
     uint8_t* dst;  // row 0 of the block, this head
     float* fac;
@@ -351,50 +361,62 @@ __global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 4 : 1024 / TG)
         fac = a.factors[kv] + (static_cast<size_t>(b) * a.Hkv + h) * a.per_seq + blk;
     }
     const float f_old = r0 > 0 ? *fac : 0.f;
-    float amax = 0.f;
-    auto take = [&](const uint4& u) {
-        float f[8];
-        unpack8<BF16>(u, f);
+    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+    // The largest magnitude's bits over the group; with infinities or NaN among them the
+    // finite ones are looked at once more, alone.
+    uint32_t top = 0;
+    bool odd = false;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        uint32_t m = 0;
+        auto take = [&](const uint4& u) {
+            m = max_magnitude2<BF16>(m, u.x, odd);
+            m = max_magnitude2<BF16>(m, u.y, odd);
+            m = max_magnitude2<BF16>(m, u.z, odd);
+            m = max_magnitude2<BF16>(m, u.w, odd);
+        };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = fabsf(f[i]);
-            amax = fmaxf(amax, x < INFINITY ? x : 0.f);
+        for (int i = 0; i < kHold; ++i)
+            if (r_first + i * kRows < rows) take(mine[i * kStride]);
+        // Blocks of more rows than are held (pages of more than kHold * kRows): read again.
+        for (int r = r_first + kHold * kRows; r < rows; r += kRows)
+            take(*reinterpret_cast<const uint4*>(src + r * a.st[kv] + c * 8));
+        top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        if constexpr (TG > 32) {
+            if (lane == 0) red[pass][warp] = top;
+            __syncthreads();  // every thread has read the old factor too
+#pragma unroll
+            for (int w = 0; w < TG / 32; ++w) top = max(top, red[pass][w]);
         }
-    };
-#pragma unroll
-    for (int i = 0; i < kHold; ++i)
-        if (r_first + i * kRows < rows) take(held[i]);
-    // Blocks past the registers' reach (pages of more than kHold * kRows rows): read twice.
-    for (int r = r_first + kHold * kRows; r < rows; r += kRows)
-        take(*reinterpret_cast<const uint4*>(src + r * a.st[kv] + c * 8));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    if constexpr (TG > 32) {
-        if (lane == 0) red[warp] = amax;
-        __syncthreads();  // every thread has read the old factor too
-#pragma unroll
-        for (int w = 0; w < TG / 32; ++w) amax = fmaxf(amax, red[w]);
+        if (odd || top < kInf) break;
+        odd = true;
     }
-    const int e = e4m3_exponent(amax);
+    const int e = e4m3_exponent(unpack_lo<BF16>(top));
     const float f_new = fmaxf(exp2_int(e), f_old);
     if (tg == 0) *fac = f_new;
     // The division by a factor the caller brought along need not be exact; by a power of
     // two the product with its inverse is.
     const bool pow2 = (__float_as_uint(f_new) & 0x7fffffu) == 0;
-    const float inv = pow2 ? 1.f / f_new : 0.f;
+    const bool plain = pow2 && !odd;
+    const float inv = 1.f / f_new;
     auto put = [&](int r, const uint4& u) {
         float f[8];
         unpack8<BF16>(u, f);
-        if (!pow2) {
+        if (plain) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= inv;
+        } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (fabsf(f[i]) < INFINITY) f[i] = f[i] / f_new;
+                f[i] = !(fabsf(f[i]) < INFINITY) ? __uint_as_float(0x7fffffffu) : pow2 ? f[i] * inv : f[i] / f_new;
         }
-        *reinterpret_cast<uint2*>(dst + static_cast<size_t>(r0 + r) * per_row + c * 8) = quantise8(f, pow2 ? inv : 1.f);
+        *reinterpret_cast<uint2*>(dst + static_cast<size_t>(r0 + r) * per_row + c * 8) =
+            make_uint2(pack4_e4m3(f[0], f[1], f[2], f[3]), pack4_e4m3(f[4], f[5], f[6], f[7]));
     };
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
-        if (r_first + i * kRows < rows) put(r_first + i * kRows, held[i]);
+        if (r_first + i * kRows < rows) put(r_first + i * kRows, mine[i * kStride]);
     for (int r = r_first + kHold * kRows; r < rows; r += kRows)
         put(r, *reinterpret_cast<const uint4*>(src + r * a.st[kv] + c * 8));
     const float ratio = f_old / f_new;
