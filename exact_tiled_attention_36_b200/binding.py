@@ -521,7 +521,7 @@ def attention_fwd_fp8(q8, k8, v8, q_scale, k_scale, v_scale, scale: float | None
 # every tensor must already have the type and the (contiguous) layout the entry point takes, and all
 # must lie on one device, which need not be the current one. `stream`: as above, a stream of that device.
 # A decode step makes these calls once per layer, next to kernels of a few microseconds, so the
-# checks are one expression per tensor and only a failing one looks for the message.
+# checks of a call are one expression and only a failing one looks for its message.
 _T = None  # torch, imported with the first call
 
 
@@ -554,14 +554,6 @@ def _need(t, name, dtype, index, shape):
     return t if _fits(t, dtype, index, shape) else _own(t, name, (dtype,), index, shape)
 
 
-def _codes(t, name, index, shape):
-    """E4M3 codes: uint8 or float8_e4m3fn."""
-    T = _torch()
-    if _fits(t, T.uint8, index, shape):
-        return t
-    return _own(t, name, (T.uint8, T.float8_e4m3fn), index, shape)
-
-
 def _call(index: int, stream, what: str, fn, *args):
     """fn(*args, stream handle) with device `index` current; its status as an exception."""
     T = _torch()
@@ -585,18 +577,31 @@ def _temporary(t, stream):
     return t
 
 
+_Pair = ctypes.c_longlong * 2
+
+
 def _rows(t, name: str, index):
-    """(token, head) strides of new rows [T, Hkv, d], any 16-byte multiples; None when contiguous."""
+    """(token, head) strides of new rows [T, Hkv, d]: any 16-byte multiples."""
     if t.dim() != 3 or not t.is_cuda or t.get_device() != index:
         raise ValueError(f"{name} must be [tokens, Hkv, d] on the CUDA device of the other tensors")
-    if t.is_contiguous():
-        return None
     st, sh, one = t.stride()
     n, H, d = t.shape
-    if one != 1:
+    if one != 1 and d > 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
     # A dimension of one element may carry any stride; it is never stepped over.
     return (st if n > 1 else H * d, sh if H > 1 else d)
+
+
+def _new_rows(k_new, v_new, index):
+    """Host arrays of the new rows' strides (kept alive by the caller's reference), and FA_BF16 or FA_FP16."""
+    T = _torch()
+    dt = k_new.dtype
+    if v_new.shape != k_new.shape or v_new.dtype is not dt:
+        raise ValueError("k_new and v_new must have one shape and type")
+    if dt is not T.bfloat16 and dt is not T.float16:
+        raise TypeError(f"k_new and v_new must be bfloat16 or float16, got {dt}")
+    return _Pair(*_rows(k_new, "k_new", index)), _Pair(*_rows(v_new, "v_new", index)), \
+        FA_BF16 if dt is T.bfloat16 else FA_FP16
 
 
 _ws_bytes = {}  # (device, sizes) -> bytes; what the library computes from the sizes and the SM count
@@ -627,45 +632,55 @@ def attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens=No
     f32, i32, dt = T.float32, T.int32, q.dtype
     index = q.get_device()
     B, Nq, Hq, d = shape = q.shape
-    if dt is not T.bfloat16 and dt is not T.float16 or index < 0 or not q.is_contiguous():
-        _own(q, "q", (T.bfloat16, T.float16), index, shape)
-    n0, n1, Hkv, _ = k_cache.shape
+    n0, n1, Hkv, _ = kshape = k_cache.shape
     paged = block_table is not None
-    kshape = (n0 if paged else B, n1, Hkv, d)
-    _codes(k_cache, "k_cache", index, kshape)
-    _codes(v_cache, "v_cache", index, kshape)
     factors = (n0, Hkv) if paged else (B, Hkv, (n1 + 127) // 128)
-    _need(k_scale, "k_scale", f32, index, factors)
-    _need(v_scale, "v_scale", f32, index, factors)
-    if cache_seqlens is not None:
-        _need(cache_seqlens, "cache_seqlens", i32, index, (B,))
-    elif paged:
-        raise ValueError("a paged cache needs cache_seqlens")
+    need = _decode_fp8_bytes(index, B, Hq, Hkv, Nq, d) if index >= 0 else 0
     if scale is None:
         scale = d ** -0.5
-    need = _decode_fp8_bytes(index, B, Hq, Hkv, Nq, d)
-    if workspace is None:
-        workspace = _temporary(T.empty(need, dtype=T.uint8, device=q.device), stream)
-    else:
-        _need(workspace, "workspace", T.uint8, index, (workspace.numel(),))
-        if workspace.numel() < need:
-            raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
     if out is None:
         out = T.empty_like(q)
-    else:
-        _need(out, "out", dt, index, shape)
     if lse is None:
         lse = T.empty((B, Hq, Nq), dtype=f32, device=q.device)
-    else:
-        _need(lse, "lse", f32, index, (B, Hq, Nq))
+    if workspace is None:
+        workspace = _temporary(T.empty(need, dtype=T.uint8, device=q.device), stream)
+    if not ((dt is T.bfloat16 or dt is T.float16) and index >= 0 and q.is_contiguous()
+            and kshape == (n0 if paged else B, n1, Hkv, d) and v_cache.shape == kshape
+            and (k_cache.dtype is T.uint8 or k_cache.dtype is T.float8_e4m3fn) and k_cache.is_contiguous()
+            and (v_cache.dtype is T.uint8 or v_cache.dtype is T.float8_e4m3fn) and v_cache.is_contiguous()
+            and k_cache.get_device() == index and v_cache.get_device() == index
+            and k_scale.dtype is f32 and k_scale.shape == factors and k_scale.is_contiguous()
+            and v_scale.dtype is f32 and v_scale.shape == factors and v_scale.is_contiguous()
+            and k_scale.get_device() == index and v_scale.get_device() == index
+            and out.dtype is dt and out.shape == shape and out.is_contiguous() and out.get_device() == index
+            and lse.dtype is f32 and lse.shape == (B, Hq, Nq) and lse.is_contiguous() and lse.get_device() == index
+            and workspace.dtype is T.uint8 and workspace.numel() >= need and workspace.is_contiguous()
+            and workspace.get_device() == index
+            and (not paged or cache_seqlens is not None and _fits(block_table, i32, index, (B, block_table.shape[-1])))
+            and (cache_seqlens is None or _fits(cache_seqlens, i32, index, (B,)))):
+        _own(q, "q", (T.bfloat16, T.float16), index, shape)
+        codes = (T.uint8, T.float8_e4m3fn)
+        _own(k_cache, "k_cache", codes, index, (n0 if paged else B, n1, Hkv, d))
+        _own(v_cache, "v_cache", codes, index, kshape)
+        _own(k_scale, "k_scale", (f32,), index, factors)
+        _own(v_scale, "v_scale", (f32,), index, factors)
+        _own(out, "out", (dt,), index, shape)
+        _own(lse, "lse", (f32,), index, (B, Hq, Nq))
+        _own(workspace, "workspace", (T.uint8,), index, workspace.shape)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
+        if cache_seqlens is not None:
+            _own(cache_seqlens, "cache_seqlens", (i32,), index, (B,))
+        if paged and cache_seqlens is None:
+            raise ValueError("a paged cache needs cache_seqlens")
+        _own(block_table, "block_table", (i32,), index, (B, block_table.shape[-1]))
     sl = None if cache_seqlens is None else cache_seqlens.data_ptr()
     code = FA_BF16 if dt is T.bfloat16 else FA_FP16
     if paged:
-        pages = block_table.shape[-1]
-        _need(block_table, "block_table", i32, index, (B, pages))
         _call(index, stream, "fa_decode_paged_fp8", lib().fa_decode_paged_fp8, q.data_ptr(), k_cache.data_ptr(),
               v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), lse.data_ptr(), sl,
-              block_table.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nq, n0, n1, pages, d, scale, bool(causal), code)
+              block_table.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nq, n0, n1, block_table.shape[1], d, scale,
+              bool(causal), code)
     else:
         _call(index, stream, "fa_decode_fp8", lib().fa_decode_fp8, q.data_ptr(), k_cache.data_ptr(),
               v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), lse.data_ptr(), sl,
@@ -705,27 +720,18 @@ def build_block_tables(cache_seqlens, new_lens, free_pages, block_table, page_si
     return slot_map, cu_new, new_seqlens, pages_used
 
 
-def _new_rows(k_new, v_new, index):
-    ks, vs = _rows(k_new, "k_new", index), _rows(v_new, "v_new", index)
-    if v_new.shape != k_new.shape or v_new.dtype is not k_new.dtype:
-        raise ValueError("k_new and v_new must have one shape and type")
-    # Host arrays of the strides (kept alive by the caller's reference).
-    pack = ctypes.c_longlong * 2
-    return None if ks is None else pack(*ks), None if vs is None else pack(*vs)
-
-
 def cache_append_paged(k_new, v_new, k_pages, v_pages, slot_map, stream=None):
     """Rows [T,Hkv,d] of k_new and v_new (any 16-byte strides) into the 16-bit page pools
     [num_pages,page_size,Hkv,d] at slot_map int32 [T]; slots outside the pool are skipped."""
     index = k_pages.get_device()
-    ks, vs = _new_rows(k_new, v_new, index)
+    ks, vs, code = _new_rows(k_new, v_new, index)
     n_new, Hkv, d = k_new.shape
     n, page = k_pages.shape[:2]
     _need(k_pages, "k_pages", k_new.dtype, index, (n, page, Hkv, d))
     _need(v_pages, "v_pages", k_new.dtype, index, (n, page, Hkv, d))
     _need(slot_map, "slot_map", _torch().int32, index, (n_new,))
     _call(index, stream, "fa_cache_append_paged", lib().fa_cache_append_paged, k_new.data_ptr(), v_new.data_ptr(), ks,
-          vs, k_pages.data_ptr(), v_pages.data_ptr(), slot_map.data_ptr(), n_new, Hkv, n, page, d, _dtype_code(k_new))
+          vs, k_pages.data_ptr(), v_pages.data_ptr(), slot_map.data_ptr(), n_new, Hkv, n, page, d, code)
 
 
 def cache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cu_new, cache_seqlens, new_seqlens,
@@ -738,27 +744,37 @@ def cache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cu_new, c
     T = _torch()
     f32, i32 = T.float32, T.int32
     index = k_cache.get_device()
-    ks, vs = _new_rows(k_new, v_new, index)
+    ks, vs, code = _new_rows(k_new, v_new, index)
     n_new, Hkv, d = k_new.shape
     B = cache_seqlens.shape[0]
     n0, n1 = k_cache.shape[:2]
     paged = block_table is not None
     kshape = (n0 if paged else B, n1, Hkv, d)
-    _codes(k_cache, "k_cache", index, kshape)
-    _codes(v_cache, "v_cache", index, kshape)
     factors = (n0, Hkv) if paged else (B, Hkv, (n1 + 127) // 128)
-    _need(k_scale, "k_scale", f32, index, factors)
-    _need(v_scale, "v_scale", f32, index, factors)
-    _need(cu_new, "cu_new", i32, index, (B + 1,))
-    _need(cache_seqlens, "cache_seqlens", i32, index, (B,))
-    _need(new_seqlens, "new_seqlens", i32, index, (B,))
-    head = (k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), cu_new.data_ptr(), cache_seqlens.data_ptr(), new_seqlens.data_ptr())
+    if not (k_cache.shape == kshape and v_cache.shape == kshape and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and (k_cache.dtype is T.uint8 or k_cache.dtype is T.float8_e4m3fn)
+            and (v_cache.dtype is T.uint8 or v_cache.dtype is T.float8_e4m3fn) and v_cache.get_device() == index
+            and k_scale.dtype is f32 and k_scale.shape == factors and k_scale.is_contiguous()
+            and v_scale.dtype is f32 and v_scale.shape == factors and v_scale.is_contiguous()
+            and k_scale.get_device() == index and v_scale.get_device() == index
+            and _fits(cu_new, i32, index, (B + 1,)) and _fits(cache_seqlens, i32, index, (B,))
+            and _fits(new_seqlens, i32, index, (B,))
+            and (not paged or _fits(block_table, i32, index, (B, block_table.shape[-1])))):
+        codes = (T.uint8, T.float8_e4m3fn)
+        _own(k_cache, "k_cache", codes, index, kshape)
+        _own(v_cache, "v_cache", codes, index, kshape)
+        _own(k_scale, "k_scale", (f32,), index, factors)
+        _own(v_scale, "v_scale", (f32,), index, factors)
+        _own(cu_new, "cu_new", (i32,), index, (B + 1,))
+        _own(cache_seqlens, "cache_seqlens", (i32,), index, (B,))
+        _own(new_seqlens, "new_seqlens", (i32,), index, (B,))
+        _own(block_table, "block_table", (i32,), index, (B, block_table.shape[-1]))
     if paged:
-        pages = block_table.shape[-1]
-        _need(block_table, "block_table", i32, index, (B, pages))
-        _call(index, stream, "fa_cache_append_paged_fp8", lib().fa_cache_append_paged_fp8, *head,
-              block_table.data_ptr(), B, n_new, max_new, Hkv, n0, n1, pages, d, _dtype_code(k_new))
+        _call(index, stream, "fa_cache_append_paged_fp8", lib().fa_cache_append_paged_fp8, k_new.data_ptr(),
+              v_new.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+              cu_new.data_ptr(), cache_seqlens.data_ptr(), new_seqlens.data_ptr(), block_table.data_ptr(), B, n_new,
+              max_new, Hkv, n0, n1, block_table.shape[1], d, code)
     else:
-        _call(index, stream, "fa_cache_append_fp8", lib().fa_cache_append_fp8, *head, B, n_new, max_new, Hkv, n1, d,
-              _dtype_code(k_new))
+        _call(index, stream, "fa_cache_append_fp8", lib().fa_cache_append_fp8, k_new.data_ptr(), v_new.data_ptr(), ks,
+              vs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), cu_new.data_ptr(),
+              cache_seqlens.data_ptr(), new_seqlens.data_ptr(), B, n_new, max_new, Hkv, n1, d, code)

@@ -303,7 +303,7 @@ __device__ __forceinline__ uint32_t rescale4_e4m3(uint32_t c, float ratio) {
 }
 
 template <bool BF16, int D, int TG>
-__global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 5 : 1280 / TG) fa_append8_kernel(const Append8Args a) {
+__global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 4 : 1024 / TG) fa_append8_kernel(const Append8Args a) {
     constexpr int kChunks = D / 8;            // 16-byte chunks of a row
     constexpr int kRows = TG / kChunks;       // rows a group reads at a time
     __shared__ uint32_t red[2][8];

@@ -160,7 +160,8 @@ def test_row_strides_of_views():
             return getattr(self.t, name)
 
     assert fb._rows(Fake(meta[:, 0]), "k", 0) == (384, 64)
-    assert fb._rows(Fake(meta[:, 0].contiguous()), "k", 0) is None
+    assert fb._rows(Fake(meta[:, 0].contiguous()), "k", 0) == (128, 64)
+    assert fb._rows(Fake(meta[:1, 0, :1]), "k", 0) == (64, 64)
     assert fb._rows(Fake(meta[:, 0, :1]), "k", 0) == (384, 64)
     with pytest.raises(ValueError, match="contiguous"):
         fb._rows(Fake(meta[:, 0].transpose(1, 2)), "k", 0)
