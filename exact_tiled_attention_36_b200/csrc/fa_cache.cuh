@@ -3,6 +3,7 @@
 // values to 16-bit and E4M3 caches.
 #pragma once
 
+#include "fa_host.h"
 #include "sm100.cuh"
 
 namespace fa {

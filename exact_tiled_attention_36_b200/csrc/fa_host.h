@@ -8,6 +8,12 @@
 
 #include "fa.h"
 
+namespace fa {
+// Device error word (beside the codes of sm100.cuh): a serving call met lengths, pages or
+// free pages that do not fit its cache; it left those tokens out.
+enum : int { kErrCacheRange = 0x4000 };
+}  // namespace fa
+
 namespace fa_host {
 
 int* error_word();     // device address of the current device's error word (null: lookup failed)

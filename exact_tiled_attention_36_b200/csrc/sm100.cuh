@@ -15,9 +15,8 @@ namespace fa {
 // shared memory window was not 1024-byte aligned (the kernel did nothing);
 // kErrSeqlenBound: a varlen sequence was longer than the max_seqlen bound the
 // caller gave (or had a negative length), so only its first max_seqlen rows or
-// keys were processed; kErrCacheRange: a serving call met lengths, pages or free pages
-// that do not fit its cache (it left those tokens out).
-enum : int { kErrTimeoutBase = 0x1000, kErrSmemAlign = 0x2000, kErrSeqlenBound = 0x3000, kErrCacheRange = 0x4000 };
+// keys were processed.
+enum : int { kErrTimeoutBase = 0x1000, kErrSmemAlign = 0x2000, kErrSeqlenBound = 0x3000 };
 
 // ---------------------------------------------------------------------------
 // generic helpers
