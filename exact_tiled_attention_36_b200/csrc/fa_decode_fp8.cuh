@@ -62,6 +62,7 @@ struct Decode8Args {
     int cap, per_seq, num_pages;       // keys a sequence can hold, its blocks, pages of the pool
     int page_size, page_box;           // rows of a page and of one TMA box (contiguous: 128)
     int HV, nch, RC;         // items of a sequence = heads (or pairs) x chunks of RC rows
+    int RT, heads;           // rows of an item's partial results, heads of an item (2: RT / 2 rows each)
     int TS, HG;              // items of a group, groups of a sequence (HV = TS HG)
     int teams;               // CTAs of the split kernel: teams x TS
     float scale_log2;
@@ -191,7 +192,7 @@ __device__ __forceinline__ bool dec8_segment(const Dec8Range& rg, const Dec8Item
 // The team's range of the T units and the item of the group that holds its first one;
 // called by every thread (it synchronises the CTA). False, for every thread, when the team
 // has none: only min(teams, T) share the units, so each of those has one at least. Uses misc + 8 .. 223.
-template <int THREADS>
+template <int THREADS, int LENS = THREADS>
 __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc, int* lens, Dec8Range& rg) {
     const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = lane_id();
     rg.team = static_cast<int>(blockIdx.x) / a.TS;
@@ -217,13 +218,13 @@ __device__ __forceinline__ bool dec8_locate(const Decode8Args& a, uint8_t* misc,
         auto units_of = [&](int b) -> long long {
             if (b >= a.B) return 0;
             const int len = dec8_len(a, b);
-            if (b < THREADS) lens[b] = len;
+            if (b < LENS) lens[b] = len;
             const int ntk = (len + 127) / 128;
             return ntk > 0 ? static_cast<long long>(a.HG) * (ntk + kDec8ItemCost) : 0;
         };
         // The first THREADS sequences are scanned while the others are only summed; a CTA whose
         // range starts further on scans on from there.
-        rg.n_lens = min(a.B, THREADS);
+        rg.n_lens = min(a.B, LENS);
         long long x = units_of(tid), rest = 0;
         for (int b = tid + THREADS; b < a.B; b += THREADS) rest += units_of(b);
         long long incl = x, run = 0;
@@ -951,10 +952,8 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
 // per row (warp w takes every eighth segment), for items split over many teams; else one
 // warp per row. A lane holds four values.
 constexpr int kDec8WideWarps = 8;
-template <int D, bool BF16, int RT, bool WIDE>
+template <int D, bool BF16, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? 32 * kDec8WideWarps : 128) fa_decode8_combine(const Decode8Args a, const int rows) {
-    constexpr bool PAIR = D == 64;
-    constexpr int RH = PAIR ? RT / 2 : RT;
     constexpr int W = WIDE ? kDec8WideWarps : 1;
     __shared__ float4 part[W][D / 4];
     const int lane = lane_id(), warp = WIDE ? warp_id() : 0;
@@ -963,8 +962,8 @@ __global__ void __launch_bounds__(WIDE ? 32 * kDec8WideWarps : 128) fa_decode8_c
     const int h = row % a.Hq, bt = row / a.Hq;
     const int t = bt % a.Nq, b = bt / a.Nq;
     const int hk = h / a.group, gr = t * a.group + h % a.group;
-    const int vh = (PAIR ? hk / 2 : hk) * a.nch + gr / a.RC;
-    const int r = (PAIR ? hk % 2 * RH : 0) + gr % a.RC;
+    const int vh = hk / a.heads * a.nch + gr / a.RC;
+    const int r = hk % a.heads * (a.RT / 2) + gr % a.RC;
     const size_t item = static_cast<size_t>(b) * a.HV + vh;
     // Launched as a programmatic dependent of the split kernel: what that wrote may be read
     // from here on.
@@ -973,8 +972,8 @@ __global__ void __launch_bounds__(WIDE ? 32 * kDec8WideWarps : 128) fa_decode8_c
     const int2 cc = a.meta[item];  // of an item without keys: anything
     const int len = dec8_len(a, b);
     const int c0 = len > 0 ? cc.x : 0, c1 = len > 0 ? cc.y : -1;
-    const size_t s0 = dec8_slot(a, 0, b, vh / a.TS, vh % a.TS) * RT + r;  // the segment of team c lies c TS RT rows further
-    const size_t step = static_cast<size_t>(a.TS) * RT;
+    // The segment of team c lies c TS RT rows further.
+    const size_t s0 = dec8_slot(a, 0, b, vh / a.TS, vh % a.TS) * a.RT + r, step = static_cast<size_t>(a.TS) * a.RT;
     const float* lp = a.lse_part + s0;
     const float4* op = reinterpret_cast<const float4*>(a.o_part + s0 * D) + lane;
     float Lm = -INFINITY, wsum = 0.f;

@@ -1,0 +1,557 @@
+// fa_decode_fp8_rows.cuh: the decode over an E4M3 cache for many query rows per KV head
+// (33 to 128: several tokens of many heads, or all heads on one KV head).
+//
+// With so many rows the transposed products of fa_decode_fp8.cuh are bound by their softmax
+// (maxima across threads, weights written byte by byte, 16 rows at a time: 347 us for 128
+// rows of 16 x 8192 keys x 8 heads). Here the rows lie along the tensor core's M = 128, one
+// row a softmax thread, as in the 16-bit kernel of fa_decode.cuh:
+//     S = Q K^T   (M = 128 rows, N = 128 keys),   O += P V   (M = 128 rows, N = d)
+// with P going through TMEM and O rescaled there when a row's maximum grows by more than
+// 2^8. The weights of a row then need a wide exponent range, which E4M3 terms do not have,
+// so this form takes its products in fp16: four warps expand the codes in shared memory
+// (exact: E4M3's values are fp16 values), the queries are scaled by a power of two into
+// fp16's range (bf16 queries exactly, within 2^-24 of a row's largest value), P is rounded
+// to fp16. The keys' block factors join each score, the values' factors P, as their share
+// of the largest one met so far (O is in units of that one and rescaled when it grows).
+//
+// Work split, segments, teams and merge: fa_decode_fp8.cuh, with one item per KV head. For
+// d = 64 a tile still loads the 128 bytes of two heads (the neighbouring CTA of the team
+// takes the other from the L2) and expands one.
+//
+// Warps: 0 TMA producer, 1 TMEM and the MMA thread, 2 block factors, 4-7 softmax, 8-11 the
+// expansion (codes, and each segment's queries). One CTA an SM: two 16-bit K and V tiles, a
+// ring of four code tiles, Q.
+#pragma once
+
+#include "fa_decode_fp8.cuh"
+
+namespace fa {
+
+template <int D>
+struct Dec8RowsCfg {
+    static constexpr int kThreads = 384;
+    static constexpr int kSlabs = D / 64;
+    static constexpr int kSlab = 128 * 128;                // 128 rows x 64 fp16 columns
+    static constexpr int kTile = kSlabs * kSlab;           // a 16-bit tile
+    static constexpr int kRaw = 128 * 128;                 // a tile of codes
+    static constexpr int kUnits = 4;                       // ring of code tiles: K, V, K, V
+    static constexpr int kScSlots = 4;
+    static constexpr int kQOff = 0;
+    static constexpr int kKOff = kQOff + kTile;
+    static constexpr int kVOff = kKOff + 2 * kTile;
+    static constexpr int kRawOff = kVOff + 2 * kTile;
+    static constexpr int kBarOff = kRawOff + kUnits * kRaw;
+    static constexpr int kNumBars = 2 * kUnits + 8 + 2 + 2 * kScSlots + 4 + 3 + 2;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 224 bytes: dec8_locate
+    static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][20]
+    static constexpr int kQfOff = kScOff + kScSlots * 20 * 4;     // float [128]: scale of a query row
+    static constexpr int kLenOff = kQfOff + 128 * 4;              // int [256]
+    static constexpr int kLens = 256;
+    static constexpr int kSmemBytes = kLenOff + kLens * 4;
+    static constexpr uint32_t kColO = 256;                        // S / P at 0 and 128
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+template <bool BF16, int D, bool PAGED>
+__global__ void __launch_bounds__(Dec8RowsCfg<D>::kThreads, 1)
+    fa_decode8_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const Decode8Args args, const int causal) {
+    using C = Dec8RowsCfg<D>;
+    constexpr int U = C::kUnits, SC = C::kScSlots;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (!smem_base_ok(smem, args.err)) return;
+    const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = lane_id();
+    uint8_t* misc = smem + C::kMiscOff;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
+    int* abort_flag = reinterpret_cast<int*>(misc + 4);
+    uint8_t* sQ = smem + C::kQOff;
+    uint8_t* sK = smem + C::kKOff;
+    uint8_t* sV = smem + C::kVOff;
+    uint8_t* raw = smem + C::kRawOff;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [U] code tiles, unit 2 g: K of tile g, 2 g + 1: V
+    uint64_t* empty = full + U;
+    uint64_t* k_full = empty + U;     // [2] expanded K of tile g in buffer g & 1
+    uint64_t* k_empty = k_full + 2;
+    uint64_t* v_full = k_empty + 2;
+    uint64_t* v_empty = v_full + 2;
+    uint64_t* q_full = v_empty + 2;   // a segment's queries
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* sc_full = q_empty + 1;  // [SC] a tile's block factors
+    uint64_t* sc_empty = sc_full + SC;
+    uint64_t* s_full = sc_empty + SC;  // [2]
+    uint64_t* p_full = s_full + 2;     // [2]
+    uint64_t* pv_done = p_full + 2;    // one completion per O += P V
+    uint64_t* o_ready = pv_done + 1;   // the segment's products are complete
+    uint64_t* o_free = o_ready + 1;    // O has been read
+    uint64_t* mma_done = o_free + 1;
+    uint64_t* sm_done = mma_done + 1;
+    float* sc = reinterpret_cast<float*>(smem + C::kScOff);
+    float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
+    const int n_warps = (args.R + 31) / 32, n_act = 32 * n_warps;  // softmax warps and threads that hold rows
+
+    // Rows of Q past R are zeros: their scores are looked at by no one but must be there.
+    for (int i = tid; i < C::kTile / 16; i += C::kThreads)
+        if ((i % (C::kSlab / 16)) / 8 >= args.R) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (tid == 0) {
+        for (int i = 0; i < U; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 128);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 128);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], n_act);
+        }
+        mbar_init(q_full, 128);
+        mbar_init(q_empty, 1 + n_warps);  // the last S product, and each softmax warp's reading of the scales
+        for (int i = 0; i < SC; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_empty[i], n_warps);
+        }
+        mbar_init(pv_done, 1);
+        mbar_init(o_ready, 1);
+        mbar_init(o_free, n_act);
+        mbar_init(mma_done, 1);
+        mbar_init(sm_done, n_act);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    // As fa_decode8_kernel: what follows reads the previous kernel's results.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    Dec8Range rg;
+    const bool work = dec8_locate<C::kThreads, C::kLens>(args, misc, reinterpret_cast<int*>(smem + C::kLenOff), rg);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+    if (!work) {
+        if (warp == 1) tmem_dealloc(tmem, 512);
+        return;
+    }
+    const WaitCtx wc{abort_flag, args.err};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        const int pb = args.page_box;
+        int u = 0;
+        bool ok = true;
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            if (lane == 0) {
+                int2* m = args.meta + (static_cast<size_t>(it.b) * args.HG + it.hg) * args.TS + rg.hl;
+                if (j0 == 0) m->x = rg.team;
+                if (j0 + n == it.ntk) m->y = rg.team;
+            }
+            const int x0 = (D == 64 ? it.hh / 2 : it.hh) * 128;  // first byte of the tile's columns
+            const int* bt = PAGED ? args.block_table + static_cast<size_t>(it.b) * args.per_seq : nullptr;
+            auto page_of = [&](int kt) {
+                const int key = kt * 128 + lane * pb;
+                return PAGED && lane * pb < 128 && key < it.len ? bt[key / args.page_size] : 0;
+            };
+            int page = page_of(j0);
+            for (int j = 0; ok && j < n; ++j) {
+                const int kt = j0 + j;
+                const int boxes = PAGED ? (min(128, it.len - kt * 128) + pb - 1) / pb : 1;
+                const int next = j + 1 < n ? page_of(kt + 1) : 0;
+                for (int kv = 0; kv < 2; ++kv, ++u) {
+                    const int st = u % U;
+                    if (!(ok = warp_all(mbar_wait(&empty[st], ((u / U) & 1) ^ 1u, wc, 140)))) break;
+                    uint8_t* dst = raw + st * C::kRaw;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(PAGED ? boxes * pb * 128 : C::kRaw));
+                    __syncwarp();
+                    const CUtensorMap* m = kv ? &tm_v : &tm_k;
+                    if (PAGED) {
+                        if (lane < boxes)
+                            tma_load_4d(dst + lane * pb * 128, m, &full[st], x0, (kt * 128 + lane * pb) % args.page_size, page, 0);
+                    } else if (lane == 0) {
+                        tma_load_4d(dst, m, &full[st], x0, kt * 128, it.b, 0);
+                    }
+                }
+                page = next;
+            }
+        }
+        // Leave no load in flight: wait for the last one issued into every buffer.
+        for (int st = 0; st < U && st < u; ++st) mbar_wait_drain(&full[st], ((u - 1 - st) / U) & 1);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_f16(128, 128, false, false, false);
+            constexpr uint32_t id_pv = idesc_f16(128, D, false, false, true);
+            const uint32_t q_addr = smem_u32(sQ);
+            auto issue_s = [&](int gg) {
+                const uint32_t k_addr = smem_u32(sK + (gg & 1) * C::kTile);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * C::kSlab + (kk & 3) * 32;
+                    mma_ss(tmem + 128 * (gg & 1), sdesc_sw128(q_addr + off, 16, 1024), sdesc_sw128(k_addr + off, 16, 1024),
+                           id_s, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(&s_full[gg & 1]);
+                tc_commit(&k_empty[gg & 1]);
+            };
+            int gk = 0, nq = 0;
+            bool ok = true;
+            for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
+                int j0, n;
+                if (!dec8_segment(rg, it, j0, n)) continue;
+                if (!(ok = mbar_wait(q_full, nq & 1, wc, 141))) break;
+                for (int j = 0; ok && j < min(n, 2); ++j) {
+                    const int gg = gk + j;
+                    if (!(ok = mbar_wait(&k_full[gg & 1], (gg >> 1) & 1, wc, 142))) break;
+                    tc_fence_after();
+                    issue_s(gg);
+                }
+                if (!ok) break;
+                if (n <= 2) tc_commit(q_empty);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int gg = gk + j, b = gg & 1;
+                    if (!(ok = mbar_wait(&v_full[b], (gg >> 1) & 1, wc, 143))) break;
+                    // O is overwritten by the segment's first P V: the previous segment's
+                    // epilogue must have read it.
+                    if (j == 0 && nq > 0 && !(ok = mbar_wait(o_free, (nq - 1) & 1, wc, 144))) break;
+                    if (!(ok = mbar_wait(&p_full[b], (gg >> 1) & 1, wc, 145))) break;
+                    tc_fence_after();
+                    const uint32_t v_addr = smem_u32(sV + b * C::kTile);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + C::kColO, tmem + 128 * b + kk * 8, sdesc_sw128(v_addr + kk * 2048, C::kSlab, 1024),
+                               id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(pv_done);
+                    tc_commit(&v_empty[b]);
+                    // S of tile gg + 2 into the columns P was just read from: one thread's
+                    // tcgen05.mma operations execute in issue order.
+                    if (j + 2 < n) {
+                        if (!(ok = mbar_wait(&k_full[b], ((gg + 2) >> 1) & 1, wc, 146))) break;
+                        tc_fence_after();
+                        issue_s(gg + 2);
+                        if (j + 3 == n) tc_commit(q_empty);
+                    }
+                }
+                tc_commit(o_ready);
+                gk += n;
+                ++nq;
+            }
+            tc_commit(mma_done);
+            mbar_wait_drain(mma_done, 0);
+            const uint32_t a = smem_u32(sm_done);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < 4000000000ull) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ block factors
+        // Lane x + 8 kv: keys 16 x .. of a tile, key or value factor. A slot holds the 8 key
+        // factors, the 8 value factors as shares of the tile's largest, and that.
+        const int x = lane & 7, kv = (lane >> 3) & 1;
+        int gk = 0;
+        bool ok = true;
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            const float* f = kv ? args.v_scale : args.k_scale;
+            auto read = [&](int kt) -> float {
+                const int key = kt * 128 + x * 16;
+                if (lane >= 16 || key >= it.len) return 0.f;
+                if constexpr (PAGED) {
+                    const int pg = args.block_table[static_cast<size_t>(it.b) * args.per_seq + key / args.page_size];
+                    return pg >= 0 && pg < args.num_pages ? f[static_cast<size_t>(pg) * args.Hkv + it.hh] : 0.f;
+                } else {
+                    return f[(static_cast<size_t>(it.b) * args.Hkv + it.hh) * args.per_seq + kt];
+                }
+            };
+            float v = read(j0);
+            for (int j = 0; j < n; ++j) {
+                const int gg = gk + j, slot = gg % SC;
+                const float next = j + 1 < n ? read(j0 + j + 1) : 0.f;
+                float top = v;
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                if (!(ok = warp_all(mbar_wait(&sc_empty[slot], ((gg / SC) & 1) ^ 1u, wc, 147)))) break;
+                float* s = sc + slot * 20;
+                // Keys without a block (past the end, pages outside the pool) have zero codes or
+                // are masked: any key factor does, but -inf times it has to stay -inf.
+                if (lane < 16) s[kv * 8 + x] = kv ? (top > 0.f ? v / top : 0.f) : (v > 0.f ? v : 1.f);
+                if (lane == 8) s[16] = top;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_full[slot]);
+                v = next;
+            }
+            gk += n;
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ expansion
+        const int t = tid - 256;
+        int gk = 0, nq = 0;
+        bool ok = true;
+        // 16 codes (a 16-byte piece) to 16 fp16 values.
+        auto expand = [](uint32_t w, uint32_t& lo, uint32_t& hi) {
+            lo = h2_of_e4m3x2(w & 0xffffu);
+            hi = h2_of_e4m3x2(w >> 16);
+        };
+        // Code tile of ring unit u into the 16-bit tile `dst`, rows from `rows` on as zeros.
+        auto tile = [&](int u, uint8_t* dst, int rows, int col0) -> bool {
+            const int st = u % U;
+            if (!warp_all(mbar_wait(&full[st], (u / U) & 1, wc, 148))) return false;
+            const uint8_t* src = raw + st * C::kRaw;
+            constexpr int P = D / 16;  // pieces of a row
+#pragma unroll 4
+            for (int i = t; i < 128 * P; i += 128) {
+                const int r = i / P, c = i % P;
+                uint4 w = *reinterpret_cast<const uint4*>(src + r * 128 + (((c + col0) ^ (r & 7)) << 4));
+                if (r >= rows) w = make_uint4(0, 0, 0, 0);
+                uint4 a, b;
+                expand(w.x, a.x, a.y);
+                expand(w.y, a.z, a.w);
+                expand(w.z, b.x, b.y);
+                expand(w.w, b.z, b.w);
+                // Values 16 c .. + 7 and + 8 ..: two 16-byte pieces of the slab's row. The lanes of the
+                // second slab store theirs in the other order (the slabs share banks).
+                uint8_t* row = dst + (c >> 2) * C::kSlab + r * 128;
+                const int p0 = 2 * (c & 3), flip = (c >> 2) & 1;
+                *reinterpret_cast<uint4*>(row + (((p0 + flip) ^ (r & 7)) << 4)) = flip ? b : a;
+                *reinterpret_cast<uint4*>(row + (((p0 + 1 - flip) ^ (r & 7)) << 4)) = flip ? a : b;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+            return true;
+        };
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            // The queries: eight lanes (d = 64) or sixteen take a row, 8 values each.
+            if (!(ok = warp_all(mbar_wait(q_empty, (nq & 1) ^ 1u, wc, 149)))) break;
+            constexpr int QP = D / 8;
+#pragma unroll 2
+            for (int i = t; i < 128 * QP; i += 128) {
+                const int r = i / QP, c = i % QP;
+                if (r - (lane / QP) >= args.R) break;  // uniform over the warp: its first row
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (r < args.R) {
+                    const size_t row = (static_cast<size_t>(it.b) * args.Nq + r / args.group) * args.Hq +
+                                       static_cast<size_t>(it.hh) * args.group + r % args.group;
+                    w = *reinterpret_cast<const uint4*>(args.q + row * D + c * 8);
+                }
+                float scale = args.scale_log2;
+                if constexpr (BF16) {
+                    float v[8], top = 0.f;
+                    unpack8<true>(w, v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
+#pragma unroll
+                    for (int off = QP / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    // The largest magnitude to [2^14, 2^15): exponents E4M3's + 9 - 15.
+                    const int e = max(e4m3_exponent(top) - 6, kMinFactorExp);
+                    const float inv = exp2_int(-e);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < INFINITY ? v[k] * inv : __uint_as_float(0x7fffffffu);
+                    w = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]),
+                                   pack2<false>(v[6], v[7]));
+                    scale *= exp2_int(e);
+                }
+                *reinterpret_cast<uint4*>(sQ + (c >> 3) * C::kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w;
+                if (c == 0) qf[r] = scale;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(q_full);
+            for (int j = 0; ok && j < n; ++j) {
+                const int gg = gk + j, b = gg & 1;
+                const int rows = min(128, it.len - (j0 + j) * 128);
+                const int col0 = D == 64 ? (it.hh & 1) * 4 : 0;
+                if (!(ok = warp_all(mbar_wait(&k_empty[b], ((gg >> 1) & 1) ^ 1u, wc, 150)))) break;
+                if (!(ok = tile(2 * gg, sK + b * C::kTile, 128, col0))) break;
+                fence_proxy_async_smem();
+                mbar_arrive(&k_full[b]);
+                // Rows of V past the sequence's end may hold anything (0 x NaN would reach O).
+                if (!(ok = warp_all(mbar_wait(&v_empty[b], ((gg >> 1) & 1) ^ 1u, wc, 151)))) break;
+                if (!(ok = tile(2 * gg + 1, sV + b * C::kTile, rows, col0))) break;
+                fence_proxy_async_smem();
+                mbar_arrive(&v_full[b]);
+            }
+            gk += n;
+            ++nq;
+        }
+    } else if (warp >= 4 && warp - 4 < n_warps) {
+        // ------------------------------------------------------------ softmax, output
+        const int w4 = warp - 4, r = w4 * 32 + lane;  // TMEM lane and query row
+        const bool live = r < args.R;
+        const int tok = live ? r / args.group : 0;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+        const uint32_t o_addr = lane_base + C::kColO;
+        int gk = 0, nq = 0;
+        bool ok = true;
+        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            const int key_hi = causal ? min(it.len, tok + it.len - args.Nq + 1) : it.len;
+            const int rel_hi = key_hi - j0 * 128;
+            ok = warp_all(mbar_wait(q_full, nq & 1, wc, 152));
+            if (!ok) break;
+            const float my_qf = live ? qf[r] : 1.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_empty);
+            float m = -INFINITY, l = 0.f, v_ref = 0.f;
+            for (int j = 0; j < n; ++j) {
+                const int gg = gk + j, b = gg & 1, slot = gg % SC;
+                ok = warp_all(mbar_wait(&sc_full[slot], (gg / SC) & 1, wc, 153));
+                if (!ok) break;
+                const float* s_sc = sc + slot * 20;
+                const float top = s_sc[16];
+                ok = warp_all(mbar_wait(&s_full[b], (gg >> 1) & 1, wc, 154));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t s_addr = lane_base + 128 * b;
+                const int lim = rel_hi - j * 128;  // columns >= lim are masked
+                // Two passes over the scores, 32 columns at a time (a thread of 384 has no
+                // registers for all 128, and unrolled the compiler holds them all). The largest
+                // scaled score first: a block's largest raw one is scaled.
+                const bool mask = __any_sync(0xffffffffu, lim < 128);
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t sv[32];
+                    tmem_ld32(s_addr + 32 * c, sv);
+                    const float2 f2 = *reinterpret_cast<const float2*>(s_sc + 2 * c);
+                    const float kf[2] = {f2.x * my_qf, f2.y * my_qf};
+                    tmem_ld_wait(sv);
+                    if (mask) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i >= lim) sv[i] = __float_as_uint(-INFINITY);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float x[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(sv[16 * g + i]);
+                        const float a = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
+                        const float b8 = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
+                        mx = fmaxf(mx, fmaxf(a, b8) * kf[g]);
+                    }
+                }
+                float alpha = 1.f;
+                bool resc = false;
+                if (mx > m + kRescaleThreshold) {
+                    if (m != -INFINITY) {
+                        alpha = ex2_approx(m - mx);
+                        resc = true;
+                    }
+                    m = mx;
+                }
+                l *= alpha;
+                // O counts in units of the largest V factor met so far.
+                if (top > v_ref) {
+                    if (v_ref > 0.f) {
+                        alpha *= v_ref / top;
+                        resc = true;
+                    }
+                    v_ref = top;
+                }
+                const float share = v_ref > 0.f ? __fdividef(top, v_ref) : 0.f;
+                const float neg_m = m == -INFINITY ? 0.f : -m;
+                const uint64_t m2 = f2_pack(neg_m, neg_m);
+                uint64_t sums[2] = {0, 0};
+                // P over the scores' columns: 32 scores become 16 columns, which were read before.
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t sv[32], pk[16];
+                    tmem_ld32(s_addr + 32 * c, sv);
+                    const float2 f2 = *reinterpret_cast<const float2*>(s_sc + 2 * c);
+                    const float2 v2 = *reinterpret_cast<const float2*>(s_sc + 8 + 2 * c);
+                    const float kf[2] = {f2.x * my_qf, f2.y * my_qf}, vs[2] = {v2.x * share, v2.y * share};
+                    tmem_ld_wait(sv);
+                    if (mask) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i >= lim) sv[i] = __float_as_uint(-INFINITY);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const uint64_t c2 = f2_pack(kf[g], kf[g]), w2 = f2_pack(vs[g], vs[g]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int k = 16 * g + 2 * i;
+                            float y0, y1, z0, z1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2, m2), y0, y1);
+                            const uint64_t p2 = f2_pack(ex2_approx(y0), ex2_approx(y1));
+                            sums[g] = f2_add(sums[g], p2);
+                            f2_unpack(f2_mul(p2, w2), z0, z1);
+                            pk[8 * g + i] = pack2<false>(z0, z1);
+                        }
+                    }
+                    tmem_st16(s_addr + 16 * c, pk);
+                }
+                l += f2_sum(f2_add(sums[0], sums[1]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_empty[slot]);
+                // Rescale O once the previous tile's P V is complete.
+                if (j > 0 && __any_sync(0xffffffffu, resc)) {
+                    ok = warp_all(mbar_wait(pv_done, (gg - 1) & 1, wc, 155));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32];
+                        tmem_ld32(o_addr + c0, ov);
+                        tmem_ld_wait(ov);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                        tmem_st32(o_addr + c0, ov);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&p_full[b]);
+            }
+            if (!ok) break;
+            ok = warp_all(mbar_wait(o_ready, nq & 1, wc, 156));
+            if (!ok) break;
+            tc_fence_after();
+            const size_t row = dec8_slot(args, rg.team, it.b, it.hg, rg.hl) * args.RT + (live ? r : 0);
+            const float inv = l == 0.f ? 0.f : __fdividef(v_ref, l);  // no key: 0; NaN stays NaN
+            float* dst = args.o_part + row * D;
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t ov[32];
+                tmem_ld32(o_addr + c0, ov);
+                tmem_ld_wait(ov);
+                if (live) {
+                    float4* d4 = reinterpret_cast<float4*>(dst + c0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d4[i] = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
+                                            __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(o_free);
+            if (live) {
+                float lg;
+                asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(l));
+                args.lse_part[row] = l == 0.f ? -INFINITY : m + lg;
+            }
+            gk += n;
+            ++nq;
+        }
+        tc_fence_before();
+        mbar_arrive(sm_done);
+    }
+}
+
+}  // namespace fa

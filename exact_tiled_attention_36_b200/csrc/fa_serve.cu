@@ -12,6 +12,7 @@
 #include "per_device.h"
 #include "fa_cache.cuh"
 #include "fa_decode_fp8.cuh"
+#include "fa_decode_fp8_rows.cuh"
 
 namespace {
 
@@ -106,10 +107,15 @@ fa_status append8(const void* k, const void* v, const long long* k_strides, cons
     return d == 64 ? launch_append8<false, 64>(a, chunks, s) : launch_append8<false, 128>(a, chunks, s);
 }
 
+// More rows of a KV head than this take the form with the rows along M.
+constexpr int kDec8ManyRows = 32;
+
 // How a call's rows become items, and its workspace: meta (each item's first and last team), the
 // partial L and O (fp32) of slots = teams x TS + items, RT rows each.
 struct Dec8Plan {
+    bool rows;    // the form with the rows along M (fa_decode8_rows_kernel)
     int rt;       // rows of a tile: the smallest of 4, 8, 16 that holds a head's (d = 64: two heads') rows
+    int heads;    // KV heads of an item
     int nch, RC;  // chunks a head's rows are cut into, and rows of a chunk
     int HV, TS;   // items of a sequence, items of a group (a team of CTAs)
     long long items, teams;
@@ -119,19 +125,27 @@ struct Dec8Plan {
 bool dec8_plan(int B, int Hq, int Hkv, int Nq, int d, Dec8Plan& p) {
     const int sms = fa_host::sm_count();
     if (sms <= 0) return false;
-    const int R = Hq / Hkv * (Nq > 0 ? Nq : 1), heads = d == 64 ? 2 : 1;
-    p.rt = heads * R <= 4 ? 4 : heads * R <= 8 ? 8 : 16;
-    const int most = p.rt / heads;
-    p.nch = (R + most - 1) / most;
-    p.RC = (R + p.nch - 1) / p.nch;
-    p.HV = (Hkv + heads - 1) / heads * p.nch;
+    const int R = Hq / Hkv * (Nq > 0 ? Nq : 1);
+    p.rows = R > kDec8ManyRows;
+    if (p.rows) {
+        p.rt = p.RC = R;
+        p.heads = p.nch = 1;
+    } else {
+        p.heads = d == 64 ? 2 : 1;
+        p.rt = p.heads * R <= 4 ? 4 : p.heads * R <= 8 ? 8 : 16;
+        const int most = p.rt / p.heads;
+        p.nch = (R + most - 1) / most;
+        p.RC = (R + p.nch - 1) / p.nch;
+    }
+    p.HV = (Hkv + p.heads - 1) / p.heads * p.nch;
     p.items = static_cast<long long>(B) * p.HV;
     // A team walks 8 items in step, or as many as divide a sequence's items evenly: 8 heads' codes
     // are 1 KB of a token, and 296 CTAs make 37 teams of 8.
     p.TS = 1;
     for (int n = 2; n <= 16 && n <= p.HV; ++n)
         if (p.HV % n == 0 && (n <= 8 || p.TS == 1)) p.TS = n;
-    p.teams = static_cast<long long>(sms) * fa::kDec8Ctas / p.TS;
+    p.teams = static_cast<long long>(sms) * (p.rows ? 1 : fa::kDec8Ctas) / p.TS;
+    if (p.teams < 1) p.teams = 1;
     const size_t slots = static_cast<size_t>(p.items + p.teams * p.TS) * p.rt;
     auto round = [](size_t x) { return (x + 255) & ~size_t(255); };
     p.meta = round(p.items * sizeof(int2));
@@ -156,11 +170,11 @@ bool kernel_ready(int smem) {
     }, &n);
 }
 
-template <bool BF16, int D, bool PAGED, int RT>
-fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode8Args& a, int causal,
-                        bool run_split, cudaStream_t s) {
-    // Both kernels launch as programmatic dependents of the one before them on the stream: the
-    // launch and the part before their griddepcontrol.wait overlap its end.
+// The split kernel and the merge, each launched as a programmatic dependent of the kernel before
+// it on the stream: the launch and the part before its griddepcontrol.wait overlap that one's end.
+template <auto Kern, bool BF16, int D>
+fa_status launch_dec8_k(int threads, int smem, const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode8Args& a,
+                        int causal, bool run_split, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -169,13 +183,11 @@ fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (run_split) {
-        constexpr auto kern = fa::fa_decode8_kernel<BF16, D == 64, PAGED, RT>;
-        using C = fa::Dec8Cfg<BF16, D == 64, RT>;
-        if (!kernel_ready<kern>(C::kSmemBytes)) return FA_ERR_CUDA;
+        if (!kernel_ready<Kern>(smem)) return FA_ERR_CUDA;
         cfg.gridDim = dim3(a.teams * a.TS);
-        cfg.blockDim = dim3(C::kThreads);
-        cfg.dynamicSmemBytes = C::kSmemBytes;
-        if (cudaLaunchKernelEx(&cfg, kern, mk, mv, a, causal) != cudaSuccess) return FA_ERR_CUDA;
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        if (cudaLaunchKernelEx(&cfg, Kern, mk, mv, a, causal) != cudaSuccess) return FA_ERR_CUDA;
     }
     // A row's segments: about teams / groups, one or two more where ranges cross.
     const int rows = a.B * a.Hq * a.Nq;
@@ -183,18 +195,30 @@ fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::
     cfg.gridDim = dim3(wide ? rows : (rows + 3) / 4);
     cfg.blockDim = dim3(wide ? 32 * fa::kDec8WideWarps : 128);
     cfg.dynamicSmemBytes = 0;
-    if ((wide ? cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT, true>, a, rows)
-              : cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, RT, false>, a, rows)) != cudaSuccess)
+    if ((wide ? cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, true>, a, rows)
+              : cudaLaunchKernelEx(&cfg, fa::fa_decode8_combine<D, BF16, false>, a, rows)) != cudaSuccess)
         return FA_ERR_CUDA;
     return launched();
 }
 
+template <bool BF16, int D, bool PAGED, int RT>
+fa_status launch_dec8_t(const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode8Args& a, int causal,
+                        bool run_split, cudaStream_t s) {
+    using C = fa::Dec8Cfg<BF16, D == 64, RT>;
+    return launch_dec8_k<fa::fa_decode8_kernel<BF16, D == 64, PAGED, RT>, BF16, D>(C::kThreads, C::kSmemBytes, mk, mv, a,
+                                                                                 causal, run_split, s);
+}
+
+// rt: rows of a tile (0: the form with the rows along M).
 template <bool BF16, int D, bool PAGED>
 fa_status launch_dec8_r(int rt, const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode8Args& a, int causal,
                         bool run_split, cudaStream_t s) {
     if (rt == 4) return launch_dec8_t<BF16, D, PAGED, 4>(mk, mv, a, causal, run_split, s);
     if (rt == 8) return launch_dec8_t<BF16, D, PAGED, 8>(mk, mv, a, causal, run_split, s);
-    return launch_dec8_t<BF16, D, PAGED, 16>(mk, mv, a, causal, run_split, s);
+    if (rt == 16) return launch_dec8_t<BF16, D, PAGED, 16>(mk, mv, a, causal, run_split, s);
+    using C = fa::Dec8RowsCfg<D>;
+    return launch_dec8_k<fa::fa_decode8_rows_kernel<BF16, D, PAGED>, BF16, D>(C::kThreads, C::kSmemBytes, mk, mv, a,
+                                                                            causal, run_split, s);
 }
 
 template <bool BF16>
@@ -274,14 +298,16 @@ fa_status decode8(const void* q, const void* k, const void* v, const float* k_sc
     a.HV = pl.HV;
     a.nch = pl.nch;
     a.RC = pl.RC;
+    a.RT = pl.rt;
+    a.heads = pl.heads;
     a.TS = pl.TS;
     a.HG = pl.HV / pl.TS;
     const long long group_tiles = tiles / pl.TS;
     a.teams = static_cast<int>(group_tiles < pl.teams ? (group_tiles > 0 ? group_tiles : 1) : pl.teams);
     a.scale_log2 = scale * kLog2e;
     const cudaStream_t s = cu(stream);
-    if (dtype == FA_BF16) return launch_dec8<true>(pl.rt, d, paged, mk, mv, a, causal, tiles > 0, s);
-    return launch_dec8<false>(pl.rt, d, paged, mk, mv, a, causal, tiles > 0, s);
+    if (dtype == FA_BF16) return launch_dec8<true>(pl.rows ? 0 : pl.rt, d, paged, mk, mv, a, causal, tiles > 0, s);
+    return launch_dec8<false>(pl.rows ? 0 : pl.rt, d, paged, mk, mv, a, causal, tiles > 0, s);
 }
 
 }  // namespace

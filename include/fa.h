@@ -435,11 +435,10 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
  * head (the block scaling of fa_fwd_fp8; "FlashAttention/zh", section "variants", names
  * FP8 and the paged cache):
  *     K[j, h, :] = k_scale(block of j, h) * e4m3(k[j, h, :]), and likewise V,
- * so a cache takes half the bytes of a 16-bit one. The queries keep their 16 bits: a
- * query is split into E4M3 terms whose sum it is (two for bf16, three for fp16; exact
- * for values within 2^-13 of the row's largest, else an error of 2^-22 of that), and so
- * is P (8 significant bits for bf16, 12 for fp16, relative to the key tile's largest
- * weight), so that both products run on the 8-bit tensor-core path. Sums are fp32.
+ * so a cache takes half the bytes of a 16-bit one. The queries keep their 16 bits: each
+ * row is scaled by a power of two and taken exactly where a value is within 2^-14 of the
+ * row's largest, else to 2^-21 of that. P is rounded to 8 significant bits for bf16 and 11
+ * for fp16 (at least; weights below 2^-17 of a tile's largest, to 2^-22 of it). Sums are fp32.
  *   q [B,Nq,Hq,d] and o (dtype), lse [B,Hq,Nq] (float32): as fa_decode.
  *   fa_decode_fp8: k, v [B,Nk,Hkv,d] E4M3 bytes; a block is 128 tokens: k_scale, v_scale
  *       DEVICE float32 [B,Hkv,ceil(Nk/128)] (the layout of fa_fwd_fp8).

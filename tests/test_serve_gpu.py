@@ -2,13 +2,15 @@
 (fa_decode_fp8, fa_decode_paged_fp8), the appends that write the caches, block tables with slot
 maps, and a run of them together.
 
-Bounds of the decode. With P relative to the key tile's largest weight, splitting it into n E4M3
-terms leaves at most 2^-4n of each weight (half a step of a 3-bit mantissa is 2^-4 of the value, of
-the first term, then of its remainder, ...; two terms for bf16, three for fp16), or 2^-22 of the
-tile's largest weight below E4M3's normal range, so
-    |O - O_ref| <= 2^-4n sum_j p_j |v_j| + half a step of the output type at O_ref + 1e-3,
-the last for the fp32 arithmetic (as for the FP8 forward) and the 2^-22 terms. L comes from the exact
-scores and keeps max|L - L_ref| <= 1e-3. Integers, codes and factors are exact."""
+Bounds of the decode. P is rounded to fp16 (half a step of 10 mantissa bits: 2^-11 of a weight); for
+bf16 up to 32 rows of a KV head it is then split into two E4M3 terms, which leave at most 2^-8 of it
+(half a step of a 3-bit mantissa is 2^-4 of the value, and so of the remainder; the three terms of fp16
+hold all 11 bits), or 2^-22 of the key tile's largest weight below E4M3's normal range (2^-25 of the
+running reference in the form for more rows, fp16 throughout), so
+    |O - O_ref| <= e sum_j p_j |v_j| + half a step of the output type at O_ref + 1e-3,
+e = 2^-8 + 2^-11 for bf16 and 2^-11 for fp16, the last for the fp32 arithmetic (as for the FP8 forward)
+and the smallest weights. L comes from the exact scores and keeps max|L - L_ref| <= 1e-3.
+Integers, codes and factors are exact."""
 import numpy as np
 import pytest
 import torch
@@ -84,8 +86,8 @@ def check_decode(o, lse, want, dtype):
     assert np.isneginf(lse[empty]).all() and (o[np.moveaxis(empty, 1, 2)] == 0).all(), "rows without keys"
     assert np.isfinite(lse[~empty]).all() and np.isfinite(o).all()
     check_l(lse[~empty], l_ref[~empty])
-    terms, step = (2, 2.0 ** -8) if dtype == torch.bfloat16 else (3, 2.0 ** -11)
-    bound = 2.0 ** (-4 * terms) * w + step * np.abs(o_ref) + 1e-3
+    e, step = (2.0 ** -8 + 2.0 ** -11, 2.0 ** -8) if dtype == torch.bfloat16 else (2.0 ** -11, 2.0 ** -11)
+    bound = e * w + step * np.abs(o_ref) + 1e-3
     err = np.abs(o - o_ref)
     record("O", err.max(), (err - bound).max())
     assert (err <= bound).all(), (err.max(), (err - bound).max())
@@ -141,6 +143,12 @@ DECODES = [
     (3, 10, 2, 3, 1200, 128, "fp16", 192, True, [1200, 193, 5]),       # pages that end inside a key tile
     (4, 8, 4, 2, 1300, 64, "bf16", 16, True, [1300, 17, 0, 1000]),
     (3, 7, 7, 1, 1280, 64, "bf16", 256, False, [1280, 257, 100]),
+    (2, 33, 1, 1, 1000, 128, "bf16", 0, False, [1000, 1]),             # just past the transposed form
+    (3, 64, 1, 2, 700, 128, "fp16", 64, True, [700, 1, 130]),          # 128 rows
+    (3, 80, 2, 1, 1500, 128, "bf16", 16, False, [1500, 0, 129]),       # 40 rows, small pages, an empty sequence
+    (2, 144, 3, 2, 640, 64, "bf16", 32, True, [640, 333]),             # 96 rows of one of two loaded heads, odd Hkv
+    (5, 32, 1, 3, 2000, 64, "fp16", 0, True, [2000, 2, 128, 1025, 0]),
+    (30, 96, 2, 1, 600, 128, "bf16", 0, False, list(range(0, 600, 20))),  # many short items
 ]
 
 
@@ -153,66 +161,74 @@ def test_decode(case):
     check_decode(o, lse, cache.reference(q, d ** -0.5, causal), q.dtype)
 
 
+@pytest.mark.parametrize("Hq", [8, 80])
 @pytest.mark.parametrize("page", [0, 16, 64])
-def test_decode_factors_of_any_value(page):
+def test_decode_factors_of_any_value(page, Hq):
     """Factors that are no powers of two and differ by 2^12 between a sequence's blocks."""
     cache = Cache(2, 1000, 2, 128, page, [1000, 413], seed=5, spread=6, factors="own")
-    q = queries(2, 1, 8, 128, "bf16", 6, 0.1)
+    q = queries(2, 1, Hq, 128, "bf16", 6, 0.1)
     o, lse = decode(cache, q, 128 ** -0.5, False)
     o_ref, l_ref, w = cache.reference(q, 128 ** -0.5, False)
-    # 2^-22 of the tile's largest weight times the largest value of the tile, 128 times
+    # 2^-22 of the tile's largest weight times the largest value of the tile, 128 times (in the form for
+    # many rows 2^-25 of the reference, which is at most 2^8 times the tile's: less)
     floor = 2.0 ** -22 * 128 * 448 * float(cache.vf.max())
     assert np.abs(f64(lse) - l_ref).max() <= 1e-3
-    assert (np.abs(f64(o) - o_ref) <= 2.0 ** -8 * (w + np.abs(o_ref)) + 1e-3 + floor).all()
+    assert (np.abs(f64(o) - o_ref) <= (2.0 ** -8 + 2.0 ** -11) * w + 2.0 ** -8 * np.abs(o_ref) + 1e-3 + floor).all()
 
 
-def test_decode_one_key_above_a_long_tail():
-    """One key 12 above 20000 others, whose small weights together still matter."""
-    B, Hq, Hkv, cap, d = 1, 4, 1, 20000, 128
+@pytest.mark.parametrize("Hq", [4, 36])
+def test_decode_one_key_above_a_long_tail(Hq):
+    """One key well above 20000 others, whose small weights together still matter."""
+    B, Hkv, cap, d = 1, 1, 20000, 128
     cache = Cache(B, cap, Hkv, d, 0, [cap], seed=8)
     q = queries(B, 1, Hq, d, "bf16", 9)
     cache.k[0, :, 0] = ref.e4m3_encode(np.zeros((cap, d)))
     cache.v[0, :, 0] = ref.e4m3_encode(np.full((cap, d), 64.0))
     cache.kf[:], cache.vf[:] = 2.0 ** -6, 2.0 ** -6
     u = f64(q)[0, 0]
-    key = u.sum(0) * 4  # q . key > 0 for every head, about 12 after scaling
-    cache.k[0, 777, 0] = ref.e4m3_encode(np.clip(key * 64 / 4, -448, 448))
+    key = u.sum(0) / max(1, Hq / 12)  # q . key about 12 after scaling (between 2 and 6 of many heads)
+    cache.k[0, 777, 0] = ref.e4m3_encode(np.clip(key * 64, -448, 448))
     cache.v[0, 777, 0] = ref.e4m3_encode(np.full(d, -64.0))
     o, lse = decode(cache, q, d ** -0.5, False)
     check_decode(o, lse, cache.reference(q, d ** -0.5, False), q.dtype)
 
 
-def test_decode_large_and_small_queries():
+@pytest.mark.parametrize("Hq", [8, 72])
+def test_decode_large_and_small_queries(Hq):
     """Query rows of very different sizes side by side, zeros among them."""
     cache = Cache(2, 500, 2, 128, 0, [500, 300], seed=10)
-    q = queries(2, 1, 8, 128, "bf16", 11)
-    q *= torch.tensor([1e-20, 1.0, 0.0, 3.0, 1e-3, 0.1, 1.0, 2.0], device="cuda").to(q.dtype)[None, None, :, None]
+    q = queries(2, 1, Hq, 128, "bf16", 11)
+    sizes = torch.tensor([1e-20, 1.0, 0.0, 3.0, 1e-3, 0.1, 1.0, 2.0] * (Hq // 8), device="cuda")
+    q *= sizes.to(q.dtype)[None, None, :, None]
     o, lse = decode(cache, q, 128 ** -0.5, False)
     check_decode(o, lse, cache.reference(q, 128 ** -0.5, False), q.dtype)
 
 
-def test_decode_nan_stays_in_its_rows():
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq", [4, 8, 80])
+def test_decode_nan_stays_in_its_rows(Hq, d):
     """A NaN in one query row, or in one KV head's keys, reaches that row or head alone."""
-    cache = Cache(2, 400, 2, 128, 64, [400, 222], seed=12)
-    q = queries(2, 1, 8, 128, "bf16", 13)
-    q[0, 0, 2, 5] = float("nan")
-    q[0, 0, 3, 5] = float("inf")
+    cache = Cache(2, 400, 2, d, 64, [400, 222], seed=12)
+    q = queries(2, 1, Hq, d, "bf16", 13)
+    q[0, 0, 0, 5] = float("nan")
+    q[0, 0, 1, 5] = float("inf")
     cache.k[cache.table[1, 1], 3, 1, 7] = 0x7F
-    o, lse = decode(cache, q, 128 ** -0.5, False)
-    bad = torch.zeros(2, 8, dtype=torch.bool)
-    bad[0, 2:4] = True
-    bad[1, 4:] = True
+    o, lse = decode(cache, q, d ** -0.5, False)
+    bad = torch.zeros(2, Hq, dtype=torch.bool)
+    bad[0, :2] = True
+    bad[1, Hq // 2:] = True
     assert torch.equal(torch.isnan(o[:, 0]).all(-1).cpu(), bad) and torch.equal(torch.isnan(o[:, 0]).any(-1).cpu(), bad)
     assert torch.equal(torch.isnan(lse[:, :, 0]).cpu(), bad)
 
 
+@pytest.mark.parametrize("Hq", [8, 70])
 @pytest.mark.parametrize("page", [16, 64])
-def test_decode_pages_outside_the_pool_read_zeros(page):
+def test_decode_pages_outside_the_pool_read_zeros(page, Hq):
     cache = Cache(3, 700, 2, 128, page, [700, 300, 650], seed=14)
     n = cache.k.shape[0]
     for b, i, pg in ((0, 1, -1), (0, 5, n), (1, 0, n + 1000), (2, 650 // page, -7)):
         cache.table[b, i] = pg
-    q = queries(3, 2, 8, 128, "bf16", 15)
+    q = queries(3, 2, Hq, 128, "bf16", 15)
     o, lse = decode(cache, q, 128 ** -0.5, True)
     check_decode(o, lse, cache.reference(q, 128 ** -0.5, True), q.dtype)
 
@@ -242,22 +258,24 @@ def test_decode_workspace_kept_between_layouts():
         check_decode(o, lse, cache.reference(q, d ** -0.5, False), q.dtype)
 
 
+@pytest.mark.parametrize("Hq", [8, 68])
 @pytest.mark.parametrize("word", [-2 ** 31, 2 ** 31 - 1, 0, -1])
-def test_decode_workspace_contents_do_not_matter(word):
+def test_decode_workspace_contents_do_not_matter(word, Hq):
     """Empty sequences among others, one of them alone, whatever the workspace holds on entry."""
     for lens, cap in (([0, 700, 0, 1, 0], 700), ([0], 128)):
         B = len(lens)
-        ws = torch.empty(fb.fa_decode_fp8_workspace_size(B, 8, 2, 1, 128) // 4, dtype=I32, device="cuda").fill_(word)
+        ws = torch.empty(fb.fa_decode_fp8_workspace_size(B, Hq, 2, 1, 128) // 4, dtype=I32, device="cuda").fill_(word)
         cache = Cache(B, cap, 2, 128, 0, lens, seed=23)
-        q = queries(B, 1, 8, 128, "bf16", 24)
+        q = queries(B, 1, Hq, 128, "bf16", 24)
         k, v, kf, vf = cache.cuda()
         o, lse = fb.attention_decode_fp8(q, k, v, kf, vf, dev(lens), workspace=ws.view(torch.uint8))
         check_decode(o, lse, cache.reference(q, 128 ** -0.5, False), q.dtype)
 
 
-def test_decode_is_deterministic_and_takes_any_stream():
+@pytest.mark.parametrize("Hq", [16, 100])
+def test_decode_is_deterministic_and_takes_any_stream(Hq):
     cache = Cache(6, 3000, 2, 128, 64, [3000, 1, 2999, 128, 1500, 777], seed=20)
-    q = queries(6, 1, 16, 128, "bf16", 21)
+    q = queries(6, 1, Hq, 128, "bf16", 21)
     k, v, kf, vf = cache.cuda()
     sl, bt = dev(cache.lens), torch.from_numpy(cache.table).cuda()
     o, lse = fb.attention_decode_fp8(q, k, v, kf, vf, sl, block_table=bt)
