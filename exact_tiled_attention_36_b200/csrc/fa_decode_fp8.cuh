@@ -342,20 +342,22 @@ __device__ __forceinline__ uint32_t h2_of_e4m3x2(uint32_t c) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
     return h;
 }
-// 16 (x - t) of a pair: exact, t being x rounded to E4M3.
+// x - t of a pair, t being x rounded to E4M3, or 16 times that: both exact.
+template <bool SCALE>
 __device__ __forceinline__ uint32_t h2_rest(uint32_t x, uint32_t t) {
     uint32_t d, r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(t));
+    if constexpr (!SCALE) return d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(0x4c004c00u));
     return r;
 }
-// The NT terms of a pair of values (fp16), each a pair of codes.
-template <int NT>
+// The NT terms of a pair of values (fp16), each a pair of codes; SCALE: term i times 16^i.
+template <int NT, bool SCALE = true>
 __device__ __forceinline__ void e4m3_terms(uint32_t x, uint32_t (&c)[NT]) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         c[i] = e4m3x2_of_h2(x);
-        if (i + 1 < NT) x = h2_rest(x, h2_of_e4m3x2(c[i]));
+        if (i + 1 < NT) x = h2_rest<SCALE>(x, h2_of_e4m3x2(c[i]));
     }
 }
 
@@ -373,33 +375,39 @@ __device__ __forceinline__ uint4 dec8_query_load(const Decode8Args& a, const Dec
                        gr % a.group;
     return *reinterpret_cast<const uint4*>(a.q + (row * C::kRowPieces + c) * 8);
 }
-template <typename C, bool BF16, bool PAIR, int RT>
-__device__ __forceinline__ void dec8_query_put(const Decode8Args& a, const uint4& raw, int i, uint8_t* dst, float* qf) {
-    constexpr int NT = C::NT;
-    const int r = i / C::kRowPieces, c = i % C::kRowPieces;
-    const int hd = PAIR ? r / C::RH : 0, rr = PAIR ? r % C::RH : r;
+// One piece of a row that LANES neighbouring lanes hold: its NT terms to at(term), 8 bytes
+// each. Returns the row's power of two.
+template <bool BF16, int LANES, int NT, bool SCALE, typename At>
+__device__ __forceinline__ float dec8_piece_put(const uint4& raw, At at) {
     float v[8];
     unpack8<BF16>(raw, v);
     float top = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
 #pragma unroll
-    for (int off = C::kRowPieces / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    for (int off = LANES / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const int e = e4m3_exponent(top);
     const float inv = exp2_int(-e);
     uint32_t t4[4][NT];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < INFINITY ? v[k] * inv : __uint_as_float(0x7fffffffu);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e4m3_terms<NT>(pack2<false>(v[2 * k], v[2 * k + 1]), t4[k]);
-    const int col = hd * 64 + c * 8;  // the piece's first byte of the tile's row
+    for (int k = 0; k < 4; ++k) e4m3_terms<NT, SCALE>(pack2<false>(v[2 * k], v[2 * k + 1]), t4[k]);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t)
+        *reinterpret_cast<uint2*>(at(t)) = make_uint2(t4[0][t] | (t4[1][t] << 16), t4[2][t] | (t4[3][t] << 16));
+    return exp2_int(e);
+}
+template <typename C, bool BF16, bool PAIR, int RT>
+__device__ __forceinline__ void dec8_query_put(const Decode8Args& a, const uint4& raw, int i, uint8_t* dst, float* qf) {
+    const int r = i / C::kRowPieces, c = i % C::kRowPieces;
+    const int hd = PAIR ? r / C::RH : 0, rr = PAIR ? r % C::RH : r;
+    const int col = hd * 64 + c * 8;  // the piece's first byte of the tile's row
+    const float scale = dec8_piece_put<BF16, C::kRowPieces, C::NT, true>(raw, [&](int t) {
         const int row = hd * C::NH + t * C::RH + rr;
-        *reinterpret_cast<uint2*>(dst + row * 128 + (((col >> 4) ^ (row & 7)) << 4) + (col & 15)) =
-            make_uint2(t4[0][t] | (t4[1][t] << 16), t4[2][t] | (t4[3][t] << 16));
-    }
-    if (c == 0) qf[r] = a.scale_log2 * exp2_int(e);
+        return dst + row * 128 + (((col >> 4) ^ (row & 7)) << 4) + (col & 15);
+    });
+    if (c == 0) qf[r] = a.scale_log2 * scale;
 }
 
 // ------------------------------------------------------------------- split kernel

@@ -7,41 +7,41 @@
 // row a softmax thread, as in the 16-bit kernel of fa_decode.cuh:
 //     S = Q K^T   (M = 128 rows, N = 128 keys),   O += P V   (M = 128 rows, N = d)
 // with P going through TMEM and O rescaled there when a row's maximum grows by more than
-// 2^8. The weights of a row then need a wide exponent range, which E4M3 terms do not have,
-// so this form takes its products in fp16: four warps expand the codes in shared memory
-// (exact: E4M3's values are fp16 values), the queries are scaled by a power of two into
-// fp16's range (bf16 queries exactly, within 2^-24 of a row's largest value), P is rounded
-// to fp16. The keys' block factors join each score, the values' factors P, as their share
-// of the largest one met so far (O is in units of that one and rescaled when it grows).
+// 2^8. S is taken from the codes as they are, a product for each of the queries' E4M3 terms
+// into the same columns (unscaled terms: exact where a value is within 2^-10 of the row's
+// largest, else to 2^-18 of that). P needs a wide exponent range, which E4M3 terms do not
+// have when a row keeps one reference: it is rounded to fp16, and four warps expand V's codes
+// to fp16 in shared memory (exact). The keys' block factors join each score, the values'
+// factors P, as their share of the largest one met so far (O is in units of that one and
+// rescaled when it grows).
 //
 // Work split, segments, teams and merge: fa_decode_fp8.cuh, with one item per KV head. For
 // d = 64 a tile still loads the 128 bytes of two heads (the neighbouring CTA of the team
-// takes the other from the L2) and expands one.
+// takes the other from the L2) and uses one.
 //
 // Warps: 0 TMA producer, 1 TMEM and the MMA thread, 2 block factors, 4-7 softmax, 8-11 the
-// expansion (codes, and each segment's queries). One CTA an SM: two 16-bit K and V tiles, a
-// ring of four code tiles, Q.
+// expansion of V and each segment's queries. One CTA an SM: two fp16 V tiles, a ring of six
+// code tiles, Q's terms.
 #pragma once
 
 #include "fa_decode_fp8.cuh"
 
 namespace fa {
 
-template <int D>
+template <bool BF16, int D>
 struct Dec8RowsCfg {
     static constexpr int kThreads = 384;
-    static constexpr int kSlabs = D / 64;
+    static constexpr int NT = BF16 ? 2 : 3;                // terms of a query
     static constexpr int kSlab = 128 * 128;                // 128 rows x 64 fp16 columns
-    static constexpr int kTile = kSlabs * kSlab;           // a 16-bit tile
-    static constexpr int kRaw = 128 * 128;                 // a tile of codes
-    static constexpr int kUnits = 4;                       // ring of code tiles: K, V, K, V
+    static constexpr int kTile = D / 64 * kSlab;           // an fp16 V tile
+    static constexpr int kRaw = 128 * 128;                 // a tile of codes, or of one term of Q
+    static constexpr int kUnits = 6;                       // ring of code tiles: K, V, K, V, ...
     static constexpr int kScSlots = 4;
     static constexpr int kQOff = 0;
-    static constexpr int kKOff = kQOff + kTile;
-    static constexpr int kVOff = kKOff + 2 * kTile;
+    static constexpr int kVOff = kQOff + NT * kRaw;
     static constexpr int kRawOff = kVOff + 2 * kTile;
     static constexpr int kBarOff = kRawOff + kUnits * kRaw;
-    static constexpr int kNumBars = 2 * kUnits + 8 + 2 + 2 * kScSlots + 4 + 3 + 2;
+    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 224 bytes: dec8_locate
     static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][20]
     static constexpr int kQfOff = kScOff + kScSlots * 20 * 4;     // float [128]: scale of a query row
@@ -49,15 +49,16 @@ struct Dec8RowsCfg {
     static constexpr int kLens = 256;
     static constexpr int kSmemBytes = kLenOff + kLens * 4;
     static constexpr uint32_t kColO = 256;                        // S / P at 0 and 128
+    static_assert(kUnits % 2 == 0, "a slot of the ring holds always K or always V");
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
 template <bool BF16, int D, bool PAGED>
-__global__ void __launch_bounds__(Dec8RowsCfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
     fa_decode8_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const Decode8Args args, const int causal) {
-    using C = Dec8RowsCfg<D>;
-    constexpr int U = C::kUnits, SC = C::kScSlots;
+    using C = Dec8RowsCfg<BF16, D>;
+    constexpr int U = C::kUnits, SC = C::kScSlots, NT = C::NT;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (!smem_base_ok(smem, args.err)) return;
     const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = lane_id();
@@ -65,14 +66,11 @@ __global__ void __launch_bounds__(Dec8RowsCfg<D>::kThreads, 1)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
     int* abort_flag = reinterpret_cast<int*>(misc + 4);
     uint8_t* sQ = smem + C::kQOff;
-    uint8_t* sK = smem + C::kKOff;
     uint8_t* sV = smem + C::kVOff;
     uint8_t* raw = smem + C::kRawOff;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [U] code tiles, unit 2 g: K of tile g, 2 g + 1: V
     uint64_t* empty = full + U;
-    uint64_t* k_full = empty + U;     // [2] expanded K of tile g in buffer g & 1
-    uint64_t* k_empty = k_full + 2;
-    uint64_t* v_full = k_empty + 2;
+    uint64_t* v_full = empty + U;     // [2] expanded V of tile g in buffer g & 1
     uint64_t* v_empty = v_full + 2;
     uint64_t* q_full = v_empty + 2;   // a segment's queries
     uint64_t* q_empty = q_full + 1;
@@ -90,17 +88,15 @@ __global__ void __launch_bounds__(Dec8RowsCfg<D>::kThreads, 1)
     const int n_warps = (args.R + 31) / 32, n_act = 32 * n_warps;  // softmax warps and threads that hold rows
 
     // Rows of Q past R are zeros: their scores are looked at by no one but must be there.
-    for (int i = tid; i < C::kTile / 16; i += C::kThreads)
-        if ((i % (C::kSlab / 16)) / 8 >= args.R) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < NT * C::kRaw / 16; i += C::kThreads)
+        if ((i % (C::kRaw / 16)) / 8 >= args.R) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (tid == 0) {
         for (int i = 0; i < U; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 4);
+            mbar_init(&empty[i], i & 1 ? 4 : 1);  // V: the expansion's warps, K: the S product
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&k_full[i], 128);
-            mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], 128);
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
@@ -189,31 +185,34 @@ __global__ void __launch_bounds__(Dec8RowsCfg<D>::kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
-            constexpr uint32_t id_s = idesc_f16(128, 128, false, false, false);
+            constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);
             constexpr uint32_t id_pv = idesc_f16(128, D, false, false, true);
             const uint32_t q_addr = smem_u32(sQ);
-            auto issue_s = [&](int gg) {
-                const uint32_t k_addr = smem_u32(sK + (gg & 1) * C::kTile);
+            // S of tile gg; col0: the head's first byte in the code rows.
+            auto issue_s = [&](int gg, uint32_t col0) {
+                const int st = (2 * gg) % U;
+                const uint32_t k_addr = smem_u32(raw + st * C::kRaw) + col0;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * C::kSlab + (kk & 3) * 32;
-                    mma_ss(tmem + 128 * (gg & 1), sdesc_sw128(q_addr + off, 16, 1024), sdesc_sw128(k_addr + off, 16, 1024),
-                           id_s, kk > 0 ? 1u : 0u);
+                for (int i = 0; i < NT * (D / 32); ++i) {
+                    const int t = i / (D / 32), kk = i % (D / 32);
+                    mma_ss_f8(tmem + 128 * (gg & 1), sdesc_sw128(q_addr + t * C::kRaw + kk * 32, 16, 1024),
+                              sdesc_sw128(k_addr + kk * 32, 16, 1024), id_s, i > 0 ? 1u : 0u);
                 }
                 tc_commit(&s_full[gg & 1]);
-                tc_commit(&k_empty[gg & 1]);
+                tc_commit(&empty[st]);
             };
             int gk = 0, nq = 0;
             bool ok = true;
             for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
                 int j0, n;
                 if (!dec8_segment(rg, it, j0, n)) continue;
+                const uint32_t col0 = D == 64 ? (it.hh & 1) * 64 : 0;
                 if (!(ok = mbar_wait(q_full, nq & 1, wc, 141))) break;
                 for (int j = 0; ok && j < min(n, 2); ++j) {
-                    const int gg = gk + j;
-                    if (!(ok = mbar_wait(&k_full[gg & 1], (gg >> 1) & 1, wc, 142))) break;
+                    const int gg = gk + j, u = 2 * gg;
+                    if (!(ok = mbar_wait(&full[u % U], (u / U) & 1, wc, 142))) break;
                     tc_fence_after();
-                    issue_s(gg);
+                    issue_s(gg, col0);
                 }
                 if (!ok) break;
                 if (n <= 2) tc_commit(q_empty);
@@ -235,9 +234,10 @@ __global__ void __launch_bounds__(Dec8RowsCfg<D>::kThreads, 1)
                     // S of tile gg + 2 into the columns P was just read from: one thread's
                     // tcgen05.mma operations execute in issue order.
                     if (j + 2 < n) {
-                        if (!(ok = mbar_wait(&k_full[b], ((gg + 2) >> 1) & 1, wc, 146))) break;
+                        const int u2 = 2 * (gg + 2);
+                        if (!(ok = mbar_wait(&full[u2 % U], (u2 / U) & 1, wc, 146))) break;
                         tc_fence_after();
-                        issue_s(gg + 2);
+                        issue_s(gg + 2, col0);
                         if (j + 3 == n) tc_commit(q_empty);
                     }
                 }
@@ -335,10 +335,10 @@ __global__ void __launch_bounds__(Dec8RowsCfg<D>::kThreads, 1)
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
-            // The queries: eight lanes (d = 64) or sixteen take a row, 8 values each.
+            // The queries' terms: eight lanes (d = 64) or sixteen take a row, 8 values each.
             if (!(ok = warp_all(mbar_wait(q_empty, (nq & 1) ^ 1u, wc, 149)))) break;
             constexpr int QP = D / 8;
-#pragma unroll 2
+#pragma unroll 1
             for (int i = t; i < 128 * QP; i += 128) {
                 const int r = i / QP, c = i % QP;
                 if (r - (lane / QP) >= args.R) break;  // uniform over the warp: its first row
@@ -348,39 +348,18 @@ __global__ void __launch_bounds__(Dec8RowsCfg<D>::kThreads, 1)
                                        static_cast<size_t>(it.hh) * args.group + r % args.group;
                     w = *reinterpret_cast<const uint4*>(args.q + row * D + c * 8);
                 }
-                float scale = args.scale_log2;
-                if constexpr (BF16) {
-                    float v[8], top = 0.f;
-                    unpack8<true>(w, v);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
-#pragma unroll
-                    for (int off = QP / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    // The largest magnitude to [2^14, 2^15): exponents E4M3's + 9 - 15.
-                    const int e = max(e4m3_exponent(top) - 6, kMinFactorExp);
-                    const float inv = exp2_int(-e);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < INFINITY ? v[k] * inv : __uint_as_float(0x7fffffffu);
-                    w = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]),
-                                   pack2<false>(v[6], v[7]));
-                    scale *= exp2_int(e);
-                }
-                *reinterpret_cast<uint4*>(sQ + (c >> 3) * C::kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w;
-                if (c == 0) qf[r] = scale;
+                const float scale = dec8_piece_put<BF16, QP, NT, false>(
+                    w, [&](int k) { return sQ + k * C::kRaw + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8; });
+                if (c == 0) qf[r] = args.scale_log2 * scale;
             }
             fence_proxy_async_smem();
             mbar_arrive(q_full);
             for (int j = 0; ok && j < n; ++j) {
                 const int gg = gk + j, b = gg & 1;
+                // Rows past the sequence's end may hold anything (0 x NaN would reach O).
                 const int rows = min(128, it.len - (j0 + j) * 128);
-                const int col0 = D == 64 ? (it.hh & 1) * 4 : 0;
-                if (!(ok = warp_all(mbar_wait(&k_empty[b], ((gg >> 1) & 1) ^ 1u, wc, 150)))) break;
-                if (!(ok = tile(2 * gg, sK + b * C::kTile, 128, col0))) break;
-                fence_proxy_async_smem();
-                mbar_arrive(&k_full[b]);
-                // Rows of V past the sequence's end may hold anything (0 x NaN would reach O).
                 if (!(ok = warp_all(mbar_wait(&v_empty[b], ((gg >> 1) & 1) ^ 1u, wc, 151)))) break;
-                if (!(ok = tile(2 * gg + 1, sV + b * C::kTile, rows, col0))) break;
+                if (!(ok = tile(2 * gg + 1, sV + b * C::kTile, rows, D == 64 ? (it.hh & 1) * 4 : 0))) break;
                 fence_proxy_async_smem();
                 mbar_arrive(&v_full[b]);
             }

@@ -216,7 +216,7 @@ fa_status launch_dec8_r(int rt, const CUtensorMap& mk, const CUtensorMap& mv, co
     if (rt == 4) return launch_dec8_t<BF16, D, PAGED, 4>(mk, mv, a, causal, run_split, s);
     if (rt == 8) return launch_dec8_t<BF16, D, PAGED, 8>(mk, mv, a, causal, run_split, s);
     if (rt == 16) return launch_dec8_t<BF16, D, PAGED, 16>(mk, mv, a, causal, run_split, s);
-    using C = fa::Dec8RowsCfg<D>;
+    using C = fa::Dec8RowsCfg<BF16, D>;
     return launch_dec8_k<fa::fa_decode8_rows_kernel<BF16, D, PAGED>, BF16, D>(C::kThreads, C::kSmemBytes, mk, mv, a,
                                                                             causal, run_split, s);
 }
