@@ -1,10 +1,11 @@
 // fa_decode_fp8_rows.cuh: the decode over an E4M3 cache for many query rows per KV head
-// (33 to 128: several tokens of many heads, or all heads on one KV head).
+// (more than 32, for d = 64 more than 24, to 128: several tokens of many heads, or many
+// heads on one KV head).
 //
 // With so many rows the transposed products of fa_decode_fp8.cuh are bound by their softmax
 // (maxima across threads, weights written byte by byte, 16 rows at a time: 347 us for 128
-// rows of 16 x 8192 keys x 8 heads). Here the rows lie along the tensor core's M = 128, one
-// row a softmax thread, as in the 16-bit kernel of fa_decode.cuh:
+// rows of 16 x 8192 keys x 8 heads). Here the rows lie along the tensor core's M = 128,
+// as in the 16-bit kernel of fa_decode.cuh, with two softmax threads a row:
 //     S = Q K^T   (M = 128 rows, N = 128 keys),   O += P V   (M = 128 rows, N = d)
 // with P going through TMEM and O rescaled there when a row's maximum grows by more than
 // 2^8. S is taken from the codes as they are, a product for each of the queries' E4M3 terms
@@ -19,9 +20,15 @@
 // d = 64 a tile still loads the 128 bytes of two heads (the neighbouring CTA of the team
 // takes the other from the L2) and uses one.
 //
-// Warps: 0 TMA producer, 1 TMEM and the MMA thread, 2 block factors, 4-7 softmax, 8-11 the
-// expansion of V and each segment's queries. One CTA an SM: two fp16 V tiles, a ring of six
-// code tiles, Q's terms.
+// Warps: 0 TMA producer, 1 TMEM and the MMA thread, 2 block factors, 4-7 and 8-11 softmax
+// (a row's first and second 64 keys of every tile, then half of its outputs; the two threads
+// exchange their maxima), 12-15 the expansion of V and each segment's queries. One CTA an
+// SM: two fp16 V tiles, a ring of six code tiles, Q's terms.
+//
+// Measured (16 x 8192 keys, 8 KV heads, d = 128, bf16): 113 us for 64 rows, 133 us for 128
+// (178 and 347 us in chunks of 16 rows). A tile takes 2,800 cycles, of which the pipe of the
+// exponentials and conversions is busy for 2,050 (two softmax warps and one of the
+// expansion on an SM sub-partition). K expanded too: 146 and 168 us.
 #pragma once
 
 #include "fa_decode_fp8.cuh"
@@ -30,7 +37,7 @@ namespace fa {
 
 template <bool BF16, int D>
 struct Dec8RowsCfg {
-    static constexpr int kThreads = 384;
+    static constexpr int kThreads = 512;
     static constexpr int NT = BF16 ? 2 : 3;                // terms of a query
     static constexpr int kSlab = 128 * 128;                // 128 rows x 64 fp16 columns
     static constexpr int kTile = D / 64 * kSlab;           // an fp16 V tile
@@ -41,11 +48,12 @@ struct Dec8RowsCfg {
     static constexpr int kVOff = kQOff + NT * kRaw;
     static constexpr int kRawOff = kVOff + 2 * kTile;
     static constexpr int kBarOff = kRawOff + kUnits * kRaw;
-    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2;
-    static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 224 bytes: dec8_locate
-    static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][20]
+    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 12;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 288 bytes: dec8_locate
+    static constexpr int kScOff = (kMiscOff + 288 + 15) / 16 * 16;  // float [slots][20]
     static constexpr int kQfOff = kScOff + kScSlots * 20 * 4;     // float [128]: scale of a query row
-    static constexpr int kLenOff = kQfOff + 128 * 4;              // int [256]
+    static constexpr int kExOff = kQfOff + 128 * 4;               // float [3][2][128]: a row's halves (two tiles' maxima, sums)
+    static constexpr int kLenOff = kExOff + 6 * 128 * 4;          // int [256]
     static constexpr int kLens = 256;
     static constexpr int kSmemBytes = kLenOff + kLens * 4;
     static constexpr uint32_t kColO = 256;                        // S / P at 0 and 128
@@ -83,9 +91,10 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
     uint64_t* o_free = o_ready + 1;    // O has been read
     uint64_t* mma_done = o_free + 1;
     uint64_t* sm_done = mma_done + 1;
+    uint64_t* pair = sm_done + 1;      // [4][3] the two warps of 32 rows: per tile parity, per segment
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
-    const int n_warps = (args.R + 31) / 32, n_act = 32 * n_warps;  // softmax warps and threads that hold rows
+    const int n_warps = (args.R + 31) / 32, n_act = 64 * n_warps;  // softmax warps of a half and threads that hold rows
 
     // Rows of Q past R are zeros: their scores are looked at by no one but must be there.
     for (int i = tid; i < NT * C::kRaw / 16; i += C::kThreads)
@@ -103,16 +112,17 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
             mbar_init(&p_full[i], n_act);
         }
         mbar_init(q_full, 128);
-        mbar_init(q_empty, 1 + n_warps);  // the last S product, and each softmax warp's reading of the scales
+        mbar_init(q_empty, 1 + 2 * n_warps);  // the last S product, and each softmax warp's reading of the scales
         for (int i = 0; i < SC; ++i) {
             mbar_init(&sc_full[i], 1);
-            mbar_init(&sc_empty[i], n_warps);
+            mbar_init(&sc_empty[i], 2 * n_warps);
         }
         mbar_init(pv_done, 1);
         mbar_init(o_ready, 1);
         mbar_init(o_free, n_act);
         mbar_init(mma_done, 1);
         mbar_init(sm_done, n_act);
+        for (int i = 0; i < 12; ++i) mbar_init(&pair[i], 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -295,9 +305,9 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
             }
             gk += n;
         }
-    } else if (warp >= 8) {
+    } else if (warp >= 12) {
         // ------------------------------------------------------------ expansion
-        const int t = tid - 256;
+        const int t = tid - 384;
         int gk = 0, nq = 0;
         bool ok = true;
         // 16 codes (a 16-byte piece) to 16 fp16 values.
@@ -366,13 +376,20 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
             gk += n;
             ++nq;
         }
-    } else if (warp >= 4 && warp - 4 < n_warps) {
+    } else if (warp >= 4 && (warp & 3) < n_warps) {
         // ------------------------------------------------------------ softmax, output
-        const int w4 = warp - 4, r = w4 * 32 + lane;  // TMEM lane and query row
+        const int w4 = warp & 3, half = (warp - 4) >> 2, r = w4 * 32 + lane;  // r: TMEM lane and query row
         const bool live = r < args.R;
         const int tok = live ? r / args.group : 0;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
-        const uint32_t o_addr = lane_base + C::kColO;
+        const uint32_t o_addr = lane_base + C::kColO + half * (D / 2);  // this thread's outputs
+        float* ex = reinterpret_cast<float*>(smem + C::kExOff);
+        uint64_t* meets = pair + 3 * w4;
+        auto meet = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            return warp_all(mbar_wait(bar, parity, wc, site));
+        };
         int gk = 0, nq = 0;
         bool ok = true;
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
@@ -390,40 +407,44 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 const int gg = gk + j, b = gg & 1, slot = gg % SC;
                 ok = warp_all(mbar_wait(&sc_full[slot], (gg / SC) & 1, wc, 153));
                 if (!ok) break;
-                const float* s_sc = sc + slot * 20;
-                const float top = s_sc[16];
+                const float* s_sc = sc + slot * 20 + 4 * half;
+                const float top = sc[slot * 20 + 16];
                 ok = warp_all(mbar_wait(&s_full[b], (gg >> 1) & 1, wc, 154));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t s_addr = lane_base + 128 * b;
-                const int lim = rel_hi - j * 128;  // columns >= lim are masked
-                // Two passes over the scores, 32 columns at a time (a thread of 384 has no
-                // registers for all 128, and unrolled the compiler holds them all). The largest
-                // scaled score first: a block's largest raw one is scaled.
-                const bool mask = __any_sync(0xffffffffu, lim < 128);
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t sv[32];
-                    tmem_ld32(s_addr + 32 * c, sv);
-                    const float2 f2 = *reinterpret_cast<const float2*>(s_sc + 2 * c);
-                    const float kf[2] = {f2.x * my_qf, f2.y * my_qf};
-                    tmem_ld_wait(sv);
-                    if (mask) {
+                const int lim = rel_hi - j * 128 - 64 * half;  // this half's columns >= lim are masked
+                uint32_t sv[2][32];
+                tmem_ld32(s_addr + 64 * half, sv[0]);
+                tmem_ld32(s_addr + 64 * half + 32, sv[1]);
+                const float4 f4 = *reinterpret_cast<const float4*>(s_sc);
+                const float4 v4 = *reinterpret_cast<const float4*>(s_sc + 8);
+                const float kf[4] = {f4.x * my_qf, f4.y * my_qf, f4.z * my_qf, f4.w * my_qf};
+                tmem_ld_wait(sv[0]);
+                tmem_ld_wait(sv[1]);
+                if (__any_sync(0xffffffffu, lim < 64)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * c + i >= lim) sv[i] = __float_as_uint(-INFINITY);
-                    }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float x[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(sv[16 * g + i]);
-                        const float a = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
-                        const float b8 = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
-                        mx = fmaxf(mx, fmaxf(a, b8) * kf[g]);
-                    }
+                    for (int i = 0; i < 64; ++i)
+                        if (i >= lim) sv[i >> 5][i & 31] = __float_as_uint(-INFINITY);
                 }
+                // The largest scaled score: a block's largest raw one is scaled.
+                float mx = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(sv[g >> 1][16 * (g & 1) + i]);
+                    const float a = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
+                    const float c = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
+                    mx = fmaxf(mx, fmaxf(a, c) * kf[g]);
+                }
+                // The row's other half (and both have read the scores' columns from here on).
+                tc_fence_before();
+                ex[(b * 2 + half) * 128 + r] = mx;
+                ok = meet(&meets[b], (gg >> 1) & 1, 157);
+                if (!ok) break;
+                tc_fence_after();
+                mx = fmaxf(mx, ex[(b * 2 + 1 - half) * 128 + r]);
                 float alpha = 1.f;
                 bool resc = false;
                 if (mx > m + kRescaleThreshold) {
@@ -445,36 +466,23 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 const float share = v_ref > 0.f ? __fdividef(top, v_ref) : 0.f;
                 const float neg_m = m == -INFINITY ? 0.f : -m;
                 const uint64_t m2 = f2_pack(neg_m, neg_m);
+                const float vs[4] = {v4.x * share, v4.y * share, v4.z * share, v4.w * share};
                 uint64_t sums[2] = {0, 0};
-                // P over the scores' columns: 32 scores become 16 columns, which were read before.
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t sv[32], pk[16];
-                    tmem_ld32(s_addr + 32 * c, sv);
-                    const float2 f2 = *reinterpret_cast<const float2*>(s_sc + 2 * c);
-                    const float2 v2 = *reinterpret_cast<const float2*>(s_sc + 8 + 2 * c);
-                    const float kf[2] = {f2.x * my_qf, f2.y * my_qf}, vs[2] = {v2.x * share, v2.y * share};
-                    tmem_ld_wait(sv);
-                    if (mask) {
+                uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * c + i >= lim) sv[i] = __float_as_uint(-INFINITY);
+                for (int g = 0; g < 4; ++g) {
+                    const uint64_t c2 = f2_pack(kf[g], kf[g]), w2 = f2_pack(vs[g], vs[g]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int k = 16 * (g & 1) + 2 * i;
+                        float y0, y1, z0, z1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[g >> 1][k]), __uint_as_float(sv[g >> 1][k + 1])), c2, m2), y0, y1);
+                        const uint64_t p2 = f2_pack(ex2_approx(y0), ex2_approx(y1));
+                        sums[g & 1] = f2_add(sums[g & 1], p2);
+                        f2_unpack(f2_mul(p2, w2), z0, z1);
+                        pk[8 * (g & 1) + i] = pack2<false>(z0, z1);
                     }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const uint64_t c2 = f2_pack(kf[g], kf[g]), w2 = f2_pack(vs[g], vs[g]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int k = 16 * g + 2 * i;
-                            float y0, y1, z0, z1;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2, m2), y0, y1);
-                            const uint64_t p2 = f2_pack(ex2_approx(y0), ex2_approx(y1));
-                            sums[g] = f2_add(sums[g], p2);
-                            f2_unpack(f2_mul(p2, w2), z0, z1);
-                            pk[8 * g + i] = pack2<false>(z0, z1);
-                        }
-                    }
-                    tmem_st16(s_addr + 16 * c, pk);
+                    if (g & 1) tmem_st16(s_addr + 32 * half + 8 * (g - 1), pk);
                 }
                 l += f2_sum(f2_add(sums[0], sums[1]));
                 __syncwarp();
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
+                    for (int c0 = 0; c0 < D / 2; c0 += 32) {
                         uint32_t ov[32];
                         tmem_ld32(o_addr + c0, ov);
                         tmem_ld_wait(ov);
@@ -499,14 +507,18 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 mbar_arrive(&p_full[b]);
             }
             if (!ok) break;
+            ex[(4 + half) * 128 + r] = l;
+            ok = meet(&meets[2], nq & 1, 158);
+            if (!ok) break;
+            l += ex[(5 - half) * 128 + r];
             ok = warp_all(mbar_wait(o_ready, nq & 1, wc, 156));
             if (!ok) break;
             tc_fence_after();
             const size_t row = dec8_slot(args, rg.team, it.b, it.hg, rg.hl) * args.RT + (live ? r : 0);
             const float inv = l == 0.f ? 0.f : __fdividef(v_ref, l);  // no key: 0; NaN stays NaN
-            float* dst = args.o_part + row * D;
+            float* dst = args.o_part + row * D + half * (D / 2);
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
+            for (int c0 = 0; c0 < D / 2; c0 += 32) {
                 uint32_t ov[32];
                 tmem_ld32(o_addr + c0, ov);
                 tmem_ld_wait(ov);
@@ -520,7 +532,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
             }
             tc_fence_before();
             mbar_arrive(o_free);
-            if (live) {
+            if (live && half == 0) {
                 float lg;
                 asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(l));
                 args.lse_part[row] = l == 0.f ? -INFINITY : m + lg;

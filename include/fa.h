@@ -436,8 +436,8 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
  * FP8 and the paged cache):
  *     K[j, h, :] = k_scale(block of j, h) * e4m3(k[j, h, :]), and likewise V,
  * so a cache takes half the bytes of a 16-bit one. The queries keep their 16 bits: each
- * row is scaled by a power of two and taken exactly where a value is within 2^-14 of the
- * row's largest, else to 2^-21 of that. P is rounded to 8 significant bits for bf16 and 11
+ * row is scaled by a power of two and taken exactly where a value is within 2^-10 of the
+ * row's largest, else to 2^-18 of that. P is rounded to 8 significant bits for bf16 and 11
  * for fp16 (at least; weights below 2^-17 of a tile's largest, to 2^-22 of it). Sums are fp32.
  *   q [B,Nq,Hq,d] and o (dtype), lse [B,Hq,Nq] (float32): as fa_decode.
  *   fa_decode_fp8: k, v [B,Nk,Hkv,d] E4M3 bytes; a block is 128 tokens: k_scale, v_scale

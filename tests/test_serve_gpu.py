@@ -3,7 +3,7 @@
 maps, and a run of them together.
 
 Bounds of the decode. P is rounded to fp16 (half a step of 10 mantissa bits: 2^-11 of a weight); for
-bf16 up to 32 rows of a KV head it is then split into two E4M3 terms, which leave at most 2^-8 of it
+bf16 up to 32 rows of a KV head (d = 64: 24) it is then split into two E4M3 terms, which leave at most 2^-8 of it
 (half a step of a 3-bit mantissa is 2^-4 of the value, and so of the remainder; the three terms of fp16
 hold all 11 bits), or 2^-22 of the key tile's largest weight below E4M3's normal range (2^-25 of the
 running reference in the form for more rows, fp16 throughout), so
@@ -143,6 +143,8 @@ DECODES = [
     (3, 10, 2, 3, 1200, 128, "fp16", 192, True, [1200, 193, 5]),       # pages that end inside a key tile
     (4, 8, 4, 2, 1300, 64, "bf16", 16, True, [1300, 17, 0, 1000]),
     (3, 7, 7, 1, 1280, 64, "bf16", 256, False, [1280, 257, 100]),
+    (2, 24, 1, 1, 500, 64, "bf16", 32, True, [500, 77]),               # three chunks of rows
+    (2, 32, 1, 1, 500, 128, "bf16", 0, False, [500, 77]),              # two, in step
     (2, 33, 1, 1, 1000, 128, "bf16", 0, False, [1000, 1]),             # just past the transposed form
     (3, 64, 1, 2, 700, 128, "fp16", 64, True, [700, 1, 130]),          # 128 rows
     (3, 80, 2, 1, 1500, 128, "bf16", 16, False, [1500, 0, 129]),       # 40 rows, small pages, an empty sequence
