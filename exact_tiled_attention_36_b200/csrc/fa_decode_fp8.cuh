@@ -36,8 +36,9 @@
 //
 // Two CTAs share an SM, so one's softmax overlaps the other's products and loads. Warp
 // roles: warp 0 TMA producer (its lanes issue the boxes of a tile), warp 1 TMEM and the
-// MMA thread, warp 2 block factors, warp 3 the queries' terms, then NW softmax warpgroups,
-// each with RT / NW of the rows (thread l: key l of every tile, then d index l of O).
+// MMA thread, warp 2 block factors, warp 3 the queries' terms and NaN among the new tokens'
+// values, then NW softmax warpgroups, each with RT / NW of the rows (thread l: key l of
+// every tile, then d index l of O).
 // With all 16 rows in one warpgroup the loop was bound by instruction fetch (2.2 warps
 // waiting for instructions per issue) and by its own latency; two halve its length.
 #pragma once
@@ -92,7 +93,7 @@ struct Dec8Cfg {
     static constexpr int kPOff = kQOff + kQB * NQ * 128;
     static constexpr int kRingOff = kPOff + 2 * N * 128;
     static constexpr int kBarOff = kRingOff + kUnits * kTile;
-    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 8 + 3 * NW;
+    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 9 + 3 * NW;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 224 bytes: dec8_locate
     static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][40]
     static constexpr int kQfOff = kScOff + kScSlots * 40 * 4;     // float [2][RT]: scale of a query row
@@ -100,8 +101,10 @@ struct Dec8Cfg {
     static constexpr int kRedOff = kQfOff + 2 * RT * 4;           // float [NW][2][4][RW]: warps' maxima
     static constexpr int kRowOff = kRedOff + 8 * RT * 4;          // float [NW][4][5][RW]: a warp's row values
     static constexpr int kSumOff = kRowOff + 20 * RT * 4;         // float [NW][4][RW]: warps' sums
-    static constexpr int kLenOff = kSumOff + 4 * RT * 4;          // int [kThreads]: lengths of the first sequences
-    static constexpr int kSmemBytes = kLenOff + kThreads * 4;
+    static constexpr int kLenOff = kSumOff + 4 * RT * 4;          // int [kLens]: lengths of the first sequences
+    static constexpr int kLens = 256;
+    static constexpr int kNanOff = kLenOff + kLens * 4;           // uint8 [3][128]: see dec8_hide_nan
+    static constexpr int kSmemBytes = kNanOff + 3 * 128;
     static constexpr uint32_t kColO = 2 * NQ;                     // S^T buffers at 0 and NQ
     static constexpr uint32_t kCols = 2 * NQ + 2 * N;
     static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
@@ -410,6 +413,25 @@ __device__ __forceinline__ void dec8_query_put(const Decode8Args& a, const uint4
     if (c == 0) qf[r] = a.scale_log2 * scale;
 }
 
+// The new tokens are seen by some rows only (causal, Nq > 1), and NaN among their values must
+// not reach the others as 0 x NaN. A warp of its own (within the softmax's loop the search cost
+// 3 %, here 1 %) looks through those rows of a V tile in shared memory before the products
+// read it: NaN codes become zeros, and `first` keeps, per byte of the tile's rows (lane: four
+// of them), the first such key, counted from `first_part` (the first key not seen by all;
+// 255: none). The rows that see that key get their NaN with the result.
+__device__ __forceinline__ void dec8_hide_nan(uint8_t* tile, int key0, int first_part, int len, uint32_t& first) {
+    const int lane = lane_id();
+#pragma unroll 1
+    for (int k = max(first_part - key0, 0); k < min(len - key0, 128); ++k) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(tile + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) + (lane & 3) * 4);
+        const uint32_t x = *w, bad = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (bad != 0) {
+            first = __vminu4(first, static_cast<uint32_t>(key0 + k - first_part) * 0x01010101u | ~bad);
+            *w = x & ~bad;
+        }
+    }
+}
+
 // ------------------------------------------------------------------- split kernel
 template <bool BF16, bool PAIR, bool PAGED, int RT>
 __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
@@ -440,8 +462,10 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     uint64_t* mma_done = pv_done + 2;
     uint64_t* sm_done = mma_done + 1;
     uint64_t* meet_bar = sm_done + 1;  // [NW][3]: a warpgroup's warps, per tile parity and per segment
+    uint64_t* v_seen = meet_bar + 3 * NW;  // a tile's values looked through by dec8_hide_nan
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
+    const bool part_seen = causal && args.Nq > 1;  // not every row sees the new tokens
 
     // Rows of P past the terms are zeros (those of Q are never looked at: their columns
     // of S^T are not read, but they must hold codes that are there).
@@ -467,6 +491,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             mbar_init(&pv_done[i], 1);
         }
         for (int i = 0; i < 3 * NW; ++i) mbar_init(&meet_bar[i], 4);
+        mbar_init(v_seen, 1);
         mbar_init(mma_done, 1);
         mbar_init(sm_done, 128 * NW);
         *abort_flag = 0;
@@ -488,7 +513,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         tmem_relinquish();
     }
     Dec8Range rg;
-    const bool work = dec8_locate<THREADS>(args, misc, reinterpret_cast<int*>(smem + C::kLenOff), rg);
+    const bool work = dec8_locate<THREADS, C::kLens>(args, misc, reinterpret_cast<int*>(smem + C::kLenOff), rg);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -564,7 +589,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 tc_commit(&s_full[gg & 1]);
                 tc_commit(&empty[(2 * gg) % U]);
             };
-            int gk = 0, nq = 0;
+            int gk = 0, nq = 0, n_seen = 0;
             bool ok = true;
             for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
                 int j0, n;
@@ -584,6 +609,9 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                     const int gg = gk + j, b = gg & 1, uv = 2 * gg + 1;
                     if (!(ok = mbar_wait(&full[uv % U], (uv / U) & 1, wc, 123))) break;
                     if (!(ok = mbar_wait(&p_full[b], (gg >> 1) & 1, wc, 124))) break;
+                    if (part_seen && (j0 + j + 1) * 128 > it.len - args.Nq + 1 &&
+                        !(ok = mbar_wait(v_seen, n_seen++ & 1, wc, 135)))
+                        break;
                     tc_fence_after();
                     const uint32_t v_addr = smem_u32(ring + (uv % U) * C::kTile);
                     const uint32_t p_addr = smem_u32(sP + b * C::N * 128);
@@ -647,7 +675,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                 if (!(ok = warp_all(mbar_wait(&sc_empty[slot], ((gg / SC) & 1) ^ 1u, wc, 126)))) break;
                 float* s = sc + slot * 40;
-                s[kv * 16 + h * 8 + x] = kv ? (top > 0.f ? v / top * 256.f : 0.f) : v;
+                s[kv * 16 + h * 8 + x] = kv && top > 0.f ? v / top * 256.f : v;  // (top 0: v is 0, or NaN to be seen)
                 if (kv == 1 && x == 0) s[32 + h] = top * (1.f / 256.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc_full[slot]);
@@ -656,8 +684,8 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             gk += n;
         }
     } else if (warp == 3) {
-        // ------------------------------------------------------------ query terms
-        int nq = 0;
+        // ------------------------------------------------------------ query terms, NaN of new tokens
+        int gk = 0, nq = 0;
         bool ok = true;
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
@@ -676,6 +704,23 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[qb]);
             }
+            const int first_part = it.len - args.Nq + 1;
+            if (part_seen && (j0 + n) * 128 > first_part) {
+                // Segment nq - 3, the last to use this part of the notes, has been read: the queries'
+                // buffer of segment nq - 2 came free after it.
+                uint32_t* noted = reinterpret_cast<uint32_t*>(smem + C::kNanOff + nq % 3 * 128) + lane;
+                uint32_t first = 0xffffffffu;
+                for (int j = max(first_part / 128 - j0, 0); j < n; ++j) {
+                    const int key0 = (j0 + j) * 128, uv = 2 * (gk + j) + 1;
+                    if (!(ok = warp_all(mbar_wait(&full[uv % U], (uv / U) & 1, wc, 136)))) break;
+                    dec8_hide_nan(ring + (uv % U) * C::kTile, key0, first_part, it.len, first);
+                    *noted = first;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_seen);
+                }
+            }
+            gk += n;
             ++nq;
         }
     } else {
@@ -925,6 +970,12 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             if (lane % (32 / RW) == 0) sums[w4 * RW + lane / (32 / RW)] = l[0];
             ok = meet(&meets[2], nq & 1, 134);
             if (!ok) break;
+            if (part_seen && (j0 + n) * 128 > all_hi) {
+                const int noted = smem[C::kNanOff + nq % 3 * 128 + l_idx];
+#pragma unroll
+                for (int r = 0; r < RW; ++r)
+                    if (row_hi[r] > all_hi + noted) acc[r] = __uint_as_float(0x7fffffffu);
+            }
             const size_t slot = dec8_slot(args, rg.team, it.b, it.hg, rg.hl);
             const int rows = min(args.RC, args.R - it.ch * args.RC);  // of each head
             auto valid = [&](int rt) {

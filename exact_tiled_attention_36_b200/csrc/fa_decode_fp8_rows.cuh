@@ -20,15 +20,16 @@
 // d = 64 a tile still loads the 128 bytes of two heads (the neighbouring CTA of the team
 // takes the other from the L2) and uses one.
 //
-// Warps: 0 TMA producer, 1 TMEM and the MMA thread, 2 block factors, 4-7 and 8-11 softmax
-// (a row's first and second 64 keys of every tile, then half of its outputs; the two threads
-// exchange their maxima), 12-15 the expansion of V and each segment's queries. One CTA an
-// SM: two fp16 V tiles, a ring of six code tiles, Q's terms.
+// Warps: 0 TMA producer, 1 TMEM and the MMA thread, 2 block factors, 3 NaN among the new
+// tokens' values, 4-7 and 8-11 softmax (a row's first and second 64 keys of every tile, then
+// half of its outputs; the two threads exchange their maxima), 12-15 the expansion of V and
+// each segment's queries. One CTA an SM: two fp16 V tiles, a ring of six code tiles, Q's
+// terms.
 //
-// Measured (16 x 8192 keys, 8 KV heads, d = 128, bf16): 113 us for 64 rows, 133 us for 128
-// (178 and 347 us in chunks of 16 rows). A tile takes 2,800 cycles, of which the pipe of the
-// exponentials and conversions is busy for 2,050 (two softmax warps and one of the
-// expansion on an SM sub-partition). K expanded too: 146 and 168 us.
+// Measured (16 x 8192 keys, 8 KV heads, d = 128, bf16): 119 us for 64 rows, 138 us for 128
+// (178 and 347 us in chunks of 16 rows); d = 64: 100 and 109 us. A tile takes 2,900 cycles, of
+// which the pipe of the exponentials and conversions is busy for 2,050 (two softmax warps and
+// one of the expansion on an SM sub-partition). K expanded too: 146 and 168 us.
 #pragma once
 
 #include "fa_decode_fp8.cuh"
@@ -48,14 +49,15 @@ struct Dec8RowsCfg {
     static constexpr int kVOff = kQOff + NT * kRaw;
     static constexpr int kRawOff = kVOff + 2 * kTile;
     static constexpr int kBarOff = kRawOff + kUnits * kRaw;
-    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 12;
+    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 12 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 288 bytes: dec8_locate
     static constexpr int kScOff = (kMiscOff + 288 + 15) / 16 * 16;  // float [slots][20]
     static constexpr int kQfOff = kScOff + kScSlots * 20 * 4;     // float [128]: scale of a query row
     static constexpr int kExOff = kQfOff + 128 * 4;               // float [3][2][128]: a row's halves (two tiles' maxima, sums)
     static constexpr int kLenOff = kExOff + 6 * 128 * 4;          // int [256]
     static constexpr int kLens = 256;
-    static constexpr int kSmemBytes = kLenOff + kLens * 4;
+    static constexpr int kNanOff = kLenOff + kLens * 4;           // uint8 [8][128]: see dec8_hide_nan
+    static constexpr int kSmemBytes = kNanOff + 8 * 128;
     static constexpr uint32_t kColO = 256;                        // S / P at 0 and 128
     static_assert(kUnits % 2 == 0, "a slot of the ring holds always K or always V");
     static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -92,8 +94,10 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
     uint64_t* mma_done = o_free + 1;
     uint64_t* sm_done = mma_done + 1;
     uint64_t* pair = sm_done + 1;      // [4][3] the two warps of 32 rows: per tile parity, per segment
+    uint64_t* v_seen = pair + 12;      // a tile's values looked through by dec8_hide_nan
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
+    const bool part_seen = causal && args.Nq > 1;  // not every row sees the new tokens
     const int n_warps = (args.R + 31) / 32, n_act = 64 * n_warps;  // softmax warps of a half and threads that hold rows
 
     // Rows of Q past R are zeros: their scores are looked at by no one but must be there.
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
         mbar_init(pv_done, 1);
         mbar_init(o_ready, 1);
         mbar_init(o_free, n_act);
+        mbar_init(v_seen, 1);
         mbar_init(mma_done, 1);
         mbar_init(sm_done, n_act);
         for (int i = 0; i < 12; ++i) mbar_init(&pair[i], 2);
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 float* s = sc + slot * 20;
                 // Keys without a block (past the end, pages outside the pool) have zero codes or
                 // are masked: any key factor does, but -inf times it has to stay -inf.
-                if (lane < 16) s[kv * 8 + x] = kv ? (top > 0.f ? v / top : 0.f) : (v > 0.f ? v : 1.f);
+                if (lane < 16) s[kv * 8 + x] = kv ? (top > 0.f ? v / top : v) : (v == 0.f ? 1.f : v);
                 if (lane == 8) s[16] = top;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc_full[slot]);
@@ -305,10 +310,35 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
             }
             gk += n;
         }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ NaN of new tokens
+        int gk = 0, nq = 0;
+        bool ok = true;
+        for (Dec8Item it = rg.first; ok && part_seen && it.P < rg.hi; it = dec8_next(args, rg, it)) {
+            int j0, n;
+            if (!dec8_segment(rg, it, j0, n)) continue;
+            const int first_part = it.len - args.Nq + 1;
+            // Segment nq - 8, the last to use this part of the notes, has been read: the ring holds V
+            // of three tiles and the products run at most two behind, so with V of tile g here the
+            // scores of tile g - 5 have been read, and the results of tiles before it.
+            uint32_t* noted = reinterpret_cast<uint32_t*>(smem + C::kNanOff + (nq & 7) * 128) + lane;
+            uint32_t first = 0xffffffffu;
+            for (int j = max(first_part / 128 - j0, 0); j < n; ++j) {
+                const int key0 = (j0 + j) * 128, u = 2 * (gk + j) + 1, st = u % U;
+                if (!(ok = warp_all(mbar_wait(&full[st], (u / U) & 1, wc, 159)))) break;
+                dec8_hide_nan(raw + st * C::kRaw, key0, first_part, it.len, first);
+                *noted = first;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_seen);
+            }
+            gk += n;
+            ++nq;
+        }
     } else if (warp >= 12) {
         // ------------------------------------------------------------ expansion
         const int t = tid - 384;
-        int gk = 0, nq = 0;
+        int gk = 0, nq = 0, n_seen = 0;
         bool ok = true;
         // 16 codes (a 16-byte piece) to 16 fp16 values.
         auto expand = [](uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -368,6 +398,9 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 const int gg = gk + j, b = gg & 1;
                 // Rows past the sequence's end may hold anything (0 x NaN would reach O).
                 const int rows = min(128, it.len - (j0 + j) * 128);
+                if (part_seen && (j0 + j + 1) * 128 > it.len - args.Nq + 1 &&
+                    !(ok = warp_all(mbar_wait(v_seen, n_seen++ & 1, wc, 160))))
+                    break;
                 if (!(ok = warp_all(mbar_wait(&v_empty[b], ((gg >> 1) & 1) ^ 1u, wc, 151)))) break;
                 if (!(ok = tile(2 * gg + 1, sV + b * C::kTile, rows, D == 64 ? (it.hh & 1) * 4 : 0))) break;
                 fence_proxy_async_smem();
@@ -396,6 +429,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
             int j0, n;
             if (!dec8_segment(rg, it, j0, n)) continue;
             const int key_hi = causal ? min(it.len, tok + it.len - args.Nq + 1) : it.len;
+            const int all_hi = it.len - args.Nq + 1;  // (causal) keys below it are seen by every row
             const int rel_hi = key_hi - j0 * 128;
             ok = warp_all(mbar_wait(q_full, nq & 1, wc, 152));
             if (!ok) break;
@@ -522,6 +556,12 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 uint32_t ov[32];
                 tmem_ld32(o_addr + c0, ov);
                 tmem_ld_wait(ov);
+                if (part_seen && (j0 + n) * 128 > all_hi) {
+                    const uint8_t* noted = smem + C::kNanOff + (nq & 7) * 128 + (D == 64 ? (it.hh & 1) * 64 : 0) + half * (D / 2) + c0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (key_hi > all_hi + noted[i]) ov[i] = 0x7fffffffu;
+                }
                 if (live) {
                     float4* d4 = reinterpret_cast<float4*>(dst + c0);
 #pragma unroll

@@ -445,6 +445,9 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
  *   fa_decode_paged_fp8: k_pages, v_pages [num_pages,page_size,Hkv,d]; a block is a page:
  *       k_scale, v_scale DEVICE float32 [num_pages,Hkv]. A block_table entry outside
  *       [0, num_pages) reads zeros.
+ *   A NaN code (an infinity or NaN that was appended) reaches the outputs of the rows that
+ *       see its key, and no others: also where only some of a causal call's rows do.
+ *   The capacity must be below 2^31 - 8192 keys (FA_ERR_UNSUPPORTED).
  *   The factors must be finite and > 0 where the sequence has tokens (not checked: they
  *       live on the device), 4-byte aligned; those of blocks past a sequence's length
  *       are not used. fa_cache_append_fp8 / fa_cache_append_paged_fp8 write both.

@@ -223,6 +223,100 @@ def test_decode_nan_stays_in_its_rows(Hq, d):
     assert torch.equal(torch.isnan(lse[:, :, 0]).cpu(), bad)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq", [2, 4, 8, 16, 36])
+@pytest.mark.parametrize("page", [0, 16])
+def test_decode_nan_values_of_new_tokens(page, Hq, d):
+    """A NaN among a new token's values (an infinity that was appended) reaches the rows that see the
+    token, at its own index, and no row before it; its key's NaN reaches their whole outputs."""
+    Hkv, Nq, cap = 2, 3, 600
+    lens = [600, 129, 257, 2, 600]
+    cache = Cache(5, cap, Hkv, d, page, lens, seed=41)
+    q = queries(5, Nq, Hq, d, "bf16", 42)
+
+    def put(x, b, pos, h, c):
+        x[(b, pos, h, c) if not page else (cache.table[b, pos // page], pos % page, h, c)] = 0xFF
+
+    place = [(0, 598, 0, 3), (0, 599, 0, 3), (0, 599, 1, d - 1), (1, 128, 1, 17), (1, 127, 0, 40), (2, 256, 0, 0),
+             (3, 1, 1, 5)]  # values: sequence, position, head, index
+    g = Hq // Hkv
+    bad = np.zeros((5, Nq, Hq, d), dtype=bool)
+    for b, pos, h, c in place:
+        for t in range(Nq):
+            bad[b, t, h * g:h * g + g, c] |= pos <= t + lens[b] - Nq
+    zero = Cache(5, cap, Hkv, d, page, lens, seed=41)  # the same with zeros there
+    for b, pos, h, c in place:
+        put(cache.v, b, pos, h, c)
+        zero.v[(b, pos, h, c) if not page else (cache.table[b, pos // page], pos % page, h, c)] = 0
+    want = zero.reference(q, d ** -0.5, True)
+    o, lse = decode(cache, q, d ** -0.5, True)
+    assert np.array_equal(np.isnan(f64(o)), bad)
+    check_decode(torch.where(torch.from_numpy(bad).cuda(), torch.from_numpy(want[0]).cuda().to(o.dtype), o), lse, want, q.dtype)
+    put(cache.k, 4, 599, 1, 9)  # a key of the last token
+    o, lse = decode(cache, q, d ** -0.5, True)
+    bad[4, 2, g:] = True
+    assert np.array_equal(np.isnan(f64(o)), bad)
+    assert np.array_equal(np.isnan(f64(lse)), np.moveaxis(bad.all(-1), 1, 2))
+
+
+@pytest.mark.parametrize("B,Hq,page", [(700, 1, 0), (700, 4, 16), (1300, 40, 16)])
+def test_decode_many_sequences(B, Hq, page):
+    """More sequences than a block has threads, most of them short or empty, long ones at the end."""
+    lens = [(7 * b) % 5 * (b % 3) for b in range(B)]
+    lens[B - 2], lens[520], lens[3] = 300, 290, 131
+    cache = Cache(B, 304, 1, 128, page, lens, seed=43)
+    q = queries(B, 1, Hq, 128, "bf16", 44)
+    o, lse = decode(cache, q, 128 ** -0.5, False)
+    check_decode(o, lse, cache.reference(q, 128 ** -0.5, False), q.dtype)
+
+
+@pytest.mark.parametrize("Hq", [8, 72])
+def test_decode_captured_behind_other_work(Hq):
+    """A captured call behind a memset, a copy and another stream's work, replayed over new contents; two
+    calls at once on two streams, each with its workspace."""
+    caches = [Cache(3, 900, 2, 128, 0, [900, 33, 512], seed=s) for s in (45, 46)]
+    q = queries(3, 1, Hq, 128, "bf16", 47)
+    data = [c.cuda() for c in caches]
+    want = [c.reference(q, 128 ** -0.5, False) for c in caches]
+    sl = dev([900, 33, 512])
+    k, v, kf, vf = (torch.empty_like(x) for x in data[0])
+    src = [x.clone() for x in data[0]]
+    side, here = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=here):
+        for x in (k, v):
+            x.zero_()  # a memset
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            for x, y in zip((v, vf), (src[1], src[3])):
+                x.copy_(y)
+        for x, y in zip((k, kf), (src[0], src[2])):
+            x.copy_(y)
+        first = fb.attention_decode_fp8(q, k, k, kf, kf, sl)
+        here.wait_stream(side)
+        out = fb.attention_decode_fp8(q, k, v, kf, vf, sl)
+        again = fb.attention_decode_fp8(q, k, v, kf, vf, sl)
+        k.zero_()  # (only after both have read it)
+    for i in (0, 1, 0):
+        for x, y in zip(src, data[i]):
+            x.copy_(y)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_decode(*out, want[i], q.dtype)
+        assert all(torch.equal(a, b) for a, b in zip(out, again)) and torch.isfinite(first[0]).all()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(10):
+        outs.append((0, fb.attention_decode_fp8(q, *data[0], sl)))
+        outs.append((1, fb.attention_decode_fp8(q, *data[1], sl, stream=side)))
+    torch.cuda.synchronize()
+    for i, (a, b) in outs:
+        check_decode(a, b, want[i], q.dtype)
+    assert fb.fa_get_last_device_error(None) == fb.FA_OK
+
+
 @pytest.mark.parametrize("Hq", [8, 70])
 @pytest.mark.parametrize("page", [16, 64])
 def test_decode_pages_outside_the_pool_read_zeros(page, Hq):
