@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 4 : 1024 / TG)
     const int i_blk = static_cast<int>(bb % a.touched), b = static_cast<int>(bb / a.touched);
     const int old = a.seqlens[b], t0 = a.cu_new[b], t1 = a.cu_new[b + 1];
     long long count = static_cast<long long>(a.new_seqlens[b]) - old;
-    const bool bad = old < 0 || count < 0 || count > a.max_new || old + count > a.cap || t0 < 0 || t1 - t0 < count ||
+    const bool bad = old < 0 || count < 0 || count > a.max_new || old + count > a.cap || t0 < 0 || static_cast<long long>(t1) - t0 < count ||
                      t0 + count > a.total_new;
     if (bad) {  // lengths that do not fit the cache or the packed tokens: the sequence is left out
         if (i_blk == 0 && h == 0 && kv == 0 && tg == 0) atomicCAS(a.err, 0, kErrCacheRange);

@@ -96,8 +96,8 @@ fa_status append8(const void* k, const void* v, const long long* k_strides, cons
     a.per_seq = per_seq;
     a.num_pages = num_pages;
     // max_new consecutive tokens touch at most 1 + ceil((max_new - 1) / unit) blocks.
-    a.touched = 1 + (a.max_new - 1 + unit - 1) / unit;
-    if (a.touched > per_seq) a.touched = per_seq;
+    const long long touched = 1 + (a.max_new - 1LL + unit - 1) / unit;
+    a.touched = touched < per_seq ? static_cast<int>(touched) : per_seq;
     a.groups = static_cast<long long>(B) * a.touched * Hkv * 2;
     a.err = fa_host::error_word();
     if (!a.err) return FA_ERR_CUDA;
@@ -247,6 +247,7 @@ fa_status decode8(const void* q, const void* k, const void* v, const float* k_sc
         if (static_cast<long long>(max_pages) * page_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     }
     const int cap = paged ? max_pages * page_size : Nk;
+    if (cap > 0x7fffffff - 8192) return FA_ERR_UNSUPPORTED;  // key indices of a tile and its boxes stay below 2^31
     if (Nq > 0 && (!q || !o || !lse || !workspace)) return FA_ERR_INVALID_ARG;
     if (cap > 0 && (!k || !v || !k_scale || !v_scale)) return FA_ERR_INVALID_ARG;
     if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) || misaligned(lse, 16) ||
@@ -256,7 +257,7 @@ fa_status decode8(const void* q, const void* k, const void* v, const float* k_sc
     fa_status st = FA_OK;
     const int g = Hq / Hkv;
     if (static_cast<long long>(g) * Nq > 128) return FA_ERR_UNSUPPORTED;
-    if (Hq > 65535 || B > 65535 || static_cast<long long>(B) * Hq * Nq > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    if (Hq > 65535 || B > 65535 || static_cast<long long>(B) * Hq * Nq > 0x7ffffff0LL) return FA_ERR_UNSUPPORTED;
     if (Nq == 0) return FA_OK;
     Dec8Plan pl;
     if (!dec8_plan(B, Hq, Hkv, Nq, d, pl)) return FA_ERR_CUDA;

@@ -41,6 +41,7 @@ def paged(**kw):
     (contiguous, dict(causal=2), INV), (contiguous, dict(d=96), UNS), (contiguous, dict(d=256), UNS),
     (contiguous, dict(dtype=5), UNS), (contiguous, dict(Hq=64, Nq=5), UNS), (contiguous, dict(B=65536), UNS),
     (contiguous, dict(q=FAKE + 8), MIS), (contiguous, dict(k=FAKE + 4), MIS), (contiguous, dict(ks=FAKE + 2), MIS),
+    (contiguous, dict(Nk=2 ** 31 - 1), UNS), (paged, dict(page=64, max_pages=2 ** 25 - 1), UNS),
     (contiguous, dict(sl=FAKE + 1), MIS), (contiguous, dict(ws=FAKE + 8), MIS), (contiguous, dict(Nq=0), OK),
     (paged, dict(sl=None), INV), (paged, dict(bt=None), INV), (paged, dict(num_pages=0), INV),
     (paged, dict(max_pages=0), INV), (paged, dict(page=8), INV), (paged, dict(page=48), UNS),
