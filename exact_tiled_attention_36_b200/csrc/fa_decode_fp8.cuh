@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
                 int j0, n;
                 if (!dec8_segment(rg, it, j0, n)) continue;
+                const int j_part = part_seen ? max(it.len - args.Nq + 1, 0) / 128 - j0 : n;  // first tile of v_seen
                 const int qb = nq % QB;
                 q_addr = smem_u32(sQ + qb * C::NQ * 128);
                 if (!(ok = mbar_wait(&q_full[qb], (nq / QB) & 1, wc, 121))) break;
@@ -608,10 +609,8 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 for (int j = 0; ok && j < n; ++j) {
                     const int gg = gk + j, b = gg & 1, uv = 2 * gg + 1;
                     if (!(ok = mbar_wait(&full[uv % U], (uv / U) & 1, wc, 123))) break;
+                    if (j >= j_part && !(ok = mbar_wait(v_seen, n_seen++ & 1, wc, 135))) break;
                     if (!(ok = mbar_wait(&p_full[b], (gg >> 1) & 1, wc, 124))) break;
-                    if (part_seen && (j0 + j + 1) * 128 > it.len - args.Nq + 1 &&
-                        !(ok = mbar_wait(v_seen, n_seen++ & 1, wc, 135)))
-                        break;
                     tc_fence_after();
                     const uint32_t v_addr = smem_u32(ring + (uv % U) * C::kTile);
                     const uint32_t p_addr = smem_u32(sP + b * C::N * 128);

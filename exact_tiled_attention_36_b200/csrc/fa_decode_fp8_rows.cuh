@@ -394,13 +394,12 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
             }
             fence_proxy_async_smem();
             mbar_arrive(q_full);
+            const int j_part = part_seen ? max(it.len - args.Nq + 1, 0) / 128 - j0 : n;  // first tile of v_seen
             for (int j = 0; ok && j < n; ++j) {
                 const int gg = gk + j, b = gg & 1;
                 // Rows past the sequence's end may hold anything (0 x NaN would reach O).
                 const int rows = min(128, it.len - (j0 + j) * 128);
-                if (part_seen && (j0 + j + 1) * 128 > it.len - args.Nq + 1 &&
-                    !(ok = warp_all(mbar_wait(v_seen, n_seen++ & 1, wc, 160))))
-                    break;
+                if (j >= j_part && !(ok = warp_all(mbar_wait(v_seen, n_seen++ & 1, wc, 160)))) break;
                 if (!(ok = warp_all(mbar_wait(&v_empty[b], ((gg >> 1) & 1) ^ 1u, wc, 151)))) break;
                 if (!(ok = tile(2 * gg + 1, sV + b * C::kTile, rows, D == 64 ? (it.hh & 1) * 4 : 0))) break;
                 fence_proxy_async_smem();
