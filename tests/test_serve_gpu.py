@@ -666,3 +666,46 @@ def test_serving_loop(d, Hkv, Hq, dtype):
                     break
         assert np.abs(f64(o16) - o_ref)[np.moveaxis(live, 1, 2)].max() <= 1e-2 + 2.0 ** -7 * np.abs(o_ref).max()
     assert taken <= pages and fb.fa_get_last_device_error(None) == fb.FA_OK
+
+
+@pytest.mark.parametrize("page", [0, 64])
+def test_offsets_past_32_bits(page):
+    """Appends to, and attention over, the end of a cache of more than 2^32 bytes of codes, against the
+    same tokens in a small cache."""
+    Hkv, d, new = 8, 128, 300
+    N = (1 << 22) + 512  # 2^32 + 2^19 bytes of keys, and of values
+    g = torch.Generator().manual_seed(48)
+    x = torch.randn(new, 2, Hkv, d, generator=g).to(torch.bfloat16).cuda()
+
+    def run(N, first):
+        """Tokens first .. first + 299 of N, the earlier ones zeros."""
+        shape = (1, N, Hkv, d) if not page else (N // page, page, Hkv, d)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in "kv")
+        fshape = (1, Hkv, -(-N // 128)) if not page else (N // page, Hkv)
+        kf, vf = (torch.ones(fshape, device="cuda") for _ in "kv")
+        bt = None
+        if page:  # a short sequence in the last pages
+            bt = torch.arange(first // page, N // page, dtype=I32, device="cuda")[None]
+            at = first % page
+        else:
+            at = first
+        fb.cache_append_fp8(x[:, 0], x[:, 1], k, v, kf, vf, dev([0, new]), dev([at]), dev([at + new]), new, block_table=bt)
+        outs = []
+        for Hq in (8, 320):
+            q = queries(1, 1, Hq, d, "bf16", 49, 20.0)  # scores far above the zeros' before
+            outs.append(fb.attention_decode_fp8(q, k, v, kf, vf, dev([at + new]), block_table=bt))
+        if page:
+            k16 = torch.zeros((max(N // 2, 512) // page, page, Hkv, d), dtype=torch.bfloat16, device="cuda")
+            n = k16.shape[0] * page
+            fb.cache_append_paged(x[:, 0], x[:, 1], k16, k16.clone(), torch.arange(n - new, n, dtype=I32, device="cuda"))
+            assert torch.equal(k16.view(-1, Hkv, d)[-new:], x[:, 0])
+        assert fb.fa_get_last_device_error(None) == fb.FA_OK
+        return k.view(-1, Hkv, d)[first:first + new].clone(), v.view(-1, Hkv, d)[first:first + new].clone(), outs
+
+    k0, v0, small = run(512, 192)
+    k1, v1, large = run(N, N - 320)
+    assert torch.equal(k0, k1) and torch.equal(v0, v1)
+    for (o0, l0), (o1, l1) in zip(small, large):
+        # the split differs, and its rounding: P to 2^-9 of itself, O to bf16
+        assert (f64(l0) > 20).all() and np.abs(f64(l0) - f64(l1)).max() <= 2e-3
+        assert np.abs(f64(o0) - f64(o1)).max() <= 2.0 ** -6 * np.abs(f64(o0)).max()
