@@ -233,9 +233,10 @@ __global__ void __launch_bounds__(256) fa_append16_kernel(const Append16Args a) 
 // One group of TG threads takes one (block, KV head, key or value): it reads the new
 // rows once, holding them (16 bytes a chunk, kHold chunks a thread) for the maximum and
 // the codes. TG is the smallest of 32, 64, 128 and 256 whose threads hold the rows a
-// block can get, so that every thread has kHold copies in flight (18,000 tokens of 8
-// heads: 31 us; 256 threads for 64-row blocks, four loads each: 45 us). They go to shared
-// memory, each thread reading back its own. The maximum is taken of the 16-bit patterns,
+// block can get, so that every thread has kHold copies in flight (when that was chosen,
+// 17,000 tokens of 8 heads took 31 us so, and 45 us with 256 threads for 64-row blocks, four
+// loads each; now 24.7 us, 64 % of the copy rate). They go to shared memory, each thread
+// reading back its own. The maximum is taken of the 16-bit patterns,
 // two at a time, and the test for infinities and NaN once per group, not per value: with
 // both in fp32 the kernel was bound by issuing instructions. Groups of a warp share CTAs
 // of eight.

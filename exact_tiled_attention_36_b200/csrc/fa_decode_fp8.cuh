@@ -71,7 +71,9 @@ struct Decode8Args {
 };
 
 constexpr int kDec8Ctas = 2;       // per SM
-constexpr int kDec8ItemCost = 1;   // units of a segment's fixed work (see kDecItemCost)
+// Units of a segment's fixed work (see kDecItemCost). 0, 1 and 2: ragged pages 47.6, 46.8 and 46.8
+// us, speculative 85.1, 84.7 and 85.3, small heads on 16-row pages 34.9, 35.1 and 36.5.
+constexpr int kDec8ItemCost = 1;
 
 template <bool BF16, bool PAIR, int RT>
 struct Dec8Cfg {
@@ -840,11 +842,15 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                         const float4 f4 = rows4(my_qf, r);
                         const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float v = __uint_as_float(s[NT - 1][r + i]);
+                        for (int i = 0; i < 4; i += 2) {  // (packed pairs further on cost registers: slower)
+                            auto two = [&](int t) {
+                                return f2_pack(__uint_as_float(s[t][r + i]), __uint_as_float(s[t][r + i + 1]));
+                            };
+                            const float kf = kMixed && r + i >= RH ? kf1 : kf0;
+                            uint64_t v = two(NT - 1);
 #pragma unroll
-                            for (int t = NT - 2; t >= 0; --t) v = fmaf(v, 0.0625f, __uint_as_float(s[t][r + i]));
-                            x[r + i] = v * f[i] * (kMixed && r + i >= RH ? kf1 : kf0);
+                            for (int t = NT - 2; t >= 0; --t) v = f2_fma(v, f2_pack(0.0625f, 0.0625f), two(t));
+                            f2_unpack(f2_mul(f2_mul(v, f2_pack(f[i], f[i + 1])), f2_pack(kf, kf)), x[r + i], x[r + i + 1]);
                         }
                     }
                 }
