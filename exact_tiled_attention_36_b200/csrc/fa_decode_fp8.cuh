@@ -44,6 +44,7 @@
 #pragma once
 
 #include "fa_cache.cuh"
+#include "notice_ring.h"
 #include "sm100.cuh"
 
 namespace fa {
@@ -95,7 +96,7 @@ struct Dec8Cfg {
     static constexpr int kPOff = kQOff + kQB * NQ * 128;
     static constexpr int kRingOff = kPOff + 2 * N * 128;
     static constexpr int kBarOff = kRingOff + kUnits * kTile;
-    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 9 + 3 * NW;
+    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 8 + 3 * NW + kNotices;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 224 bytes: dec8_locate
     static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][40]
     static constexpr int kQfOff = kScOff + kScSlots * 40 * 4;     // float [2][RT]: scale of a query row
@@ -112,6 +113,7 @@ struct Dec8Cfg {
     static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
     static_assert(kQPieces <= 128 * NW && kQPieces % 32 == 0, "one piece a softmax thread, whole warps");
     static_assert(kCols <= 256, "two CTAs share the SM's 512 columns");
+    static_assert(kNotices >= ring_values(kUnits), "a notice barrier per value tile the ring holds");
     static_assert(kRingOff % 1024 == 0 && kPOff % 1024 == 0, "swizzle atoms");
     static_assert(kSmemBytes <= 115712, "two CTAs share the SM's shared memory");
 };
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     uint64_t* mma_done = pv_done + 2;
     uint64_t* sm_done = mma_done + 1;
     uint64_t* meet_bar = sm_done + 1;  // [NW][3]: a warpgroup's warps, per tile parity and per segment
-    uint64_t* v_seen = meet_bar + 3 * NW;  // a tile's values looked through by dec8_hide_nan
+    uint64_t* v_seen = meet_bar + 3 * NW;  // [kNotices] a tile's values looked through by dec8_hide_nan
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
     const bool part_seen = causal && args.Nq > 1;  // not every row sees the new tokens
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             mbar_init(&pv_done[i], 1);
         }
         for (int i = 0; i < 3 * NW; ++i) mbar_init(&meet_bar[i], 4);
-        mbar_init(v_seen, 1);
+        for (int i = 0; i < kNotices; ++i) mbar_init(&v_seen[i], 1);
         mbar_init(mma_done, 1);
         mbar_init(sm_done, 128 * NW);
         *abort_flag = 0;
@@ -611,7 +613,10 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 for (int j = 0; ok && j < n; ++j) {
                     const int gg = gk + j, b = gg & 1, uv = 2 * gg + 1;
                     if (!(ok = mbar_wait(&full[uv % U], (uv / U) & 1, wc, 123))) break;
-                    if (j >= j_part && !(ok = mbar_wait(v_seen, n_seen++ & 1, wc, 135))) break;
+                    if (j >= j_part) {
+                        if (!(ok = mbar_wait(&v_seen[notice_bar(n_seen)], notice_parity(n_seen), wc, 135))) break;
+                        ++n_seen;
+                    }
                     if (!(ok = mbar_wait(&p_full[b], (gg >> 1) & 1, wc, 124))) break;
                     tc_fence_after();
                     const uint32_t v_addr = smem_u32(ring + (uv % U) * C::kTile);
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ query terms, NaN of new tokens
-        int gk = 0, nq = 0;
+        int gk = 0, nq = 0, n_told = 0;
         bool ok = true;
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
@@ -718,7 +723,8 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                     *noted = first;
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(v_seen);
+                    if (lane == 0) mbar_arrive(&v_seen[notice_bar(n_told)]);
+                    ++n_told;
                 }
             }
             gk += n;

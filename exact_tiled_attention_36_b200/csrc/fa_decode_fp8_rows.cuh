@@ -49,7 +49,7 @@ struct Dec8RowsCfg {
     static constexpr int kVOff = kQOff + NT * kRaw;
     static constexpr int kRawOff = kVOff + 2 * kTile;
     static constexpr int kBarOff = kRawOff + kUnits * kRaw;
-    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 12 + 1;
+    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 12 + kNotices;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 288 bytes: dec8_locate
     static constexpr int kScOff = (kMiscOff + 288 + 15) / 16 * 16;  // float [slots][20]
     static constexpr int kQfOff = kScOff + kScSlots * 20 * 4;     // float [128]: scale of a query row
@@ -60,6 +60,7 @@ struct Dec8RowsCfg {
     static constexpr int kSmemBytes = kNanOff + 8 * 128;
     static constexpr uint32_t kColO = 256;                        // S / P at 0 and 128
     static_assert(kUnits % 2 == 0, "a slot of the ring holds always K or always V");
+    static_assert(kNotices >= ring_values(kUnits), "a notice barrier per value tile the ring holds");
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
     uint64_t* mma_done = o_free + 1;
     uint64_t* sm_done = mma_done + 1;
     uint64_t* pair = sm_done + 1;      // [4][3] the two warps of 32 rows: per tile parity, per segment
-    uint64_t* v_seen = pair + 12;      // a tile's values looked through by dec8_hide_nan
+    uint64_t* v_seen = pair + 12;      // [kNotices] a tile's values looked through by dec8_hide_nan
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
     const bool part_seen = causal && args.Nq > 1;  // not every row sees the new tokens
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
         mbar_init(pv_done, 1);
         mbar_init(o_ready, 1);
         mbar_init(o_free, n_act);
-        mbar_init(v_seen, 1);
+        for (int i = 0; i < kNotices; ++i) mbar_init(&v_seen[i], 1);
         mbar_init(mma_done, 1);
         mbar_init(sm_done, n_act);
         for (int i = 0; i < 12; ++i) mbar_init(&pair[i], 2);
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ NaN of new tokens
-        int gk = 0, nq = 0;
+        int gk = 0, nq = 0, n_told = 0;
         bool ok = true;
         for (Dec8Item it = rg.first; ok && part_seen && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
@@ -330,7 +331,8 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 *noted = first;
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(v_seen);
+                if (lane == 0) mbar_arrive(&v_seen[notice_bar(n_told)]);
+                ++n_told;
             }
             gk += n;
             ++nq;
@@ -399,7 +401,10 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 const int gg = gk + j, b = gg & 1;
                 // Rows past the sequence's end may hold anything (0 x NaN would reach O).
                 const int rows = min(128, it.len - (j0 + j) * 128);
-                if (j >= j_part && !(ok = warp_all(mbar_wait(v_seen, n_seen++ & 1, wc, 160)))) break;
+                if (j >= j_part) {
+                    if (!(ok = warp_all(mbar_wait(&v_seen[notice_bar(n_seen)], notice_parity(n_seen), wc, 160)))) break;
+                    ++n_seen;
+                }
                 if (!(ok = warp_all(mbar_wait(&v_empty[b], ((gg >> 1) & 1) ^ 1u, wc, 151)))) break;
                 if (!(ok = tile(2 * gg + 1, sV + b * C::kTile, rows, D == 64 ? (it.hh & 1) * 4 : 0))) break;
                 fence_proxy_async_smem();
