@@ -96,7 +96,7 @@ struct Dec8Cfg {
     static constexpr int kPOff = kQOff + kQB * NQ * 128;
     static constexpr int kRingOff = kPOff + 2 * N * 128;
     static constexpr int kBarOff = kRingOff + kUnits * kTile;
-    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 8 + 3 * NW + kNotices;
+    static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 8 + 3 * NW + 2 * kNotices;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 224 bytes: dec8_locate
     static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][40]
     static constexpr int kQfOff = kScOff + kScSlots * 40 * 4;     // float [2][RT]: scale of a query row
@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     uint64_t* sm_done = mma_done + 1;
     uint64_t* meet_bar = sm_done + 1;  // [NW][3]: a warpgroup's warps, per tile parity and per segment
     uint64_t* v_seen = meet_bar + 3 * NW;  // [kNotices] a tile's values looked through by dec8_hide_nan
+    uint64_t* v_due = v_seen + kNotices;   // [kNotices] the load of such a tile has begun
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
     const bool part_seen = causal && args.Nq > 1;  // not every row sees the new tokens
@@ -495,7 +496,10 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
             mbar_init(&pv_done[i], 1);
         }
         for (int i = 0; i < 3 * NW; ++i) mbar_init(&meet_bar[i], 4);
-        for (int i = 0; i < kNotices; ++i) mbar_init(&v_seen[i], 1);
+        for (int i = 0; i < kNotices; ++i) {
+            mbar_init(&v_seen[i], 1);
+            mbar_init(&v_due[i], 1);
+        }
         mbar_init(mma_done, 1);
         mbar_init(sm_done, 128 * NW);
         *abort_flag = 0;
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         // page that holds them (a page outside the pool: zeros). Boxes past the sequence's
         // end are not loaded.
         const int pb = args.page_box;
-        int u = 0;
+        int u = 0, n_due = 0;
         bool ok = true;
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
@@ -551,6 +555,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 return PAGED && lane * pb < 128 && key < it.len ? bt[key / args.page_size] : 0;
             };
             int page = page_of(j0);
+            const int kt_part = part_seen ? max(it.len - args.Nq + 1, 0) / 128 : it.ntk;  // first tile of v_due
             for (int j = 0; ok && j < n; ++j) {
                 const int kt = j0 + j;
                 const int boxes = PAGED ? (min(128, it.len - kt * 128) + pb - 1) / pb : 1;
@@ -560,6 +565,10 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                     if (!(ok = warp_all(mbar_wait(&empty[st], ((u / U) & 1) ^ 1u, wc, 120)))) break;
                     uint8_t* dst = ring + st * C::kTile;
                     if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(PAGED ? boxes * pb * 128 : C::kTile));
+                    if (kv && kt >= kt_part) {
+                        if (lane == 0) mbar_arrive(&v_due[notice_bar(n_due)]);
+                        ++n_due;
+                    }
                     __syncwarp();
                     const CUtensorMap* m = kv ? &tm_v : &tm_k;
                     if (PAGED) {
@@ -718,6 +727,7 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 uint32_t first = 0xffffffffu;
                 for (int j = max(first_part / 128 - j0, 0); j < n; ++j) {
                     const int key0 = (j0 + j) * 128, uv = 2 * (gk + j) + 1;
+                    if (!(ok = warp_all(mbar_wait(&v_due[notice_bar(n_told)], notice_parity(n_told), wc, 137)))) break;
                     if (!(ok = warp_all(mbar_wait(&full[uv % U], (uv / U) & 1, wc, 136)))) break;
                     dec8_hide_nan(ring + (uv % U) * C::kTile, key0, first_part, it.len, first);
                     *noted = first;

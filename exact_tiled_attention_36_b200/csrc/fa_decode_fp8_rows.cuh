@@ -49,7 +49,7 @@ struct Dec8RowsCfg {
     static constexpr int kVOff = kQOff + NT * kRaw;
     static constexpr int kRawOff = kVOff + 2 * kTile;
     static constexpr int kBarOff = kRawOff + kUnits * kRaw;
-    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 12 + kNotices;
+    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 12 + 2 * kNotices;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 288 bytes: dec8_locate
     static constexpr int kScOff = (kMiscOff + 288 + 15) / 16 * 16;  // float [slots][20]
     static constexpr int kQfOff = kScOff + kScSlots * 20 * 4;     // float [128]: scale of a query row
@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
     uint64_t* sm_done = mma_done + 1;
     uint64_t* pair = sm_done + 1;      // [4][3] the two warps of 32 rows: per tile parity, per segment
     uint64_t* v_seen = pair + 12;      // [kNotices] a tile's values looked through by dec8_hide_nan
+    uint64_t* v_due = v_seen + kNotices;  // [kNotices] the load of such a tile has begun
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
     const bool part_seen = causal && args.Nq > 1;  // not every row sees the new tokens
@@ -125,7 +126,10 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
         mbar_init(pv_done, 1);
         mbar_init(o_ready, 1);
         mbar_init(o_free, n_act);
-        for (int i = 0; i < kNotices; ++i) mbar_init(&v_seen[i], 1);
+        for (int i = 0; i < kNotices; ++i) {
+            mbar_init(&v_seen[i], 1);
+            mbar_init(&v_due[i], 1);
+        }
         mbar_init(mma_done, 1);
         mbar_init(sm_done, n_act);
         for (int i = 0; i < 12; ++i) mbar_init(&pair[i], 2);
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         const int pb = args.page_box;
-        int u = 0;
+        int u = 0, n_due = 0;
         bool ok = true;
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
@@ -175,6 +179,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 return PAGED && lane * pb < 128 && key < it.len ? bt[key / args.page_size] : 0;
             };
             int page = page_of(j0);
+            const int kt_part = part_seen ? max(it.len - args.Nq + 1, 0) / 128 : it.ntk;  // first tile of v_due
             for (int j = 0; ok && j < n; ++j) {
                 const int kt = j0 + j;
                 const int boxes = PAGED ? (min(128, it.len - kt * 128) + pb - 1) / pb : 1;
@@ -184,6 +189,10 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                     if (!(ok = warp_all(mbar_wait(&empty[st], ((u / U) & 1) ^ 1u, wc, 140)))) break;
                     uint8_t* dst = raw + st * C::kRaw;
                     if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(PAGED ? boxes * pb * 128 : C::kRaw));
+                    if (kv && kt >= kt_part) {
+                        if (lane == 0) mbar_arrive(&v_due[notice_bar(n_due)]);
+                        ++n_due;
+                    }
                     __syncwarp();
                     const CUtensorMap* m = kv ? &tm_v : &tm_k;
                     if (PAGED) {
@@ -326,6 +335,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
             uint32_t first = 0xffffffffu;
             for (int j = max(first_part / 128 - j0, 0); j < n; ++j) {
                 const int key0 = (j0 + j) * 128, u = 2 * (gk + j) + 1, st = u % U;
+                if (!(ok = warp_all(mbar_wait(&v_due[notice_bar(n_told)], notice_parity(n_told), wc, 161)))) break;
                 if (!(ok = warp_all(mbar_wait(&full[st], (u / U) & 1, wc, 159)))) break;
                 dec8_hide_nan(raw + st * C::kRaw, key0, first_part, it.len, first);
                 *noted = first;

@@ -22,5 +22,6 @@ def test_both_kernels_take_the_barriers_from_the_header():
         src = open(os.path.join(CSRC, name)).read()
         assert "kNotices >= ring_values(kUnits)" in src, name
         assert len(re.findall(r"v_seen\[notice_bar\(\w+\)\]", src)) == 2, name  # the notice, the wait
-        assert len(re.findall(r"notice_parity\(\w+\)", src)) == 1, name
-        assert not re.search(r"mbar_(arrive|wait)\(v_seen\b(?!\[)", src), name
+        assert len(re.findall(r"v_due\[notice_bar\(\w+\)\]", src)) == 2, name
+        assert len(re.findall(r"notice_parity\(\w+\)", src)) == 2, name
+        assert not re.search(r"mbar_(arrive|wait)\(v_(seen|due)\b(?!\[)", src), name
