@@ -17,8 +17,10 @@ arguments; every step of the computation runs in the library's kernels.
 
 ``attention_fwd``, ``attention_varlen_fwd`` and ``attention_bwd`` are the
 same calls on torch CUDA tensors: torch allocates the outputs and workspace,
-the library fills them. There is no fallback: if ``libfa.so`` is missing or
-a call fails, an exception is raised.
+the library fills them. With ``stream`` they run, allocate and convert on that
+stream, whichever is current: inputs and given outputs must be ready for it, and the
+caller orders other streams' use of the results. There is no fallback: if ``libfa.so``
+is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
@@ -382,6 +384,29 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_stream(stream, device, fn, *args, **given):
+    """fn(*args, **given) with `stream` (a torch stream or a handle) current, so that what it allocates and
+    converts comes from that stream's memory and in its order: a block of another stream's memory may still
+    be in use by that one's earlier work. A result that fn made may be used on the stream that was current,
+    too: once dropped, its memory is kept until what that stream was given so far has run."""
+    import torch
+    if device.type != "cuda":
+        return fn(*args, **given)  # refused there
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is one of {stream.device}, the tensors are on {device}")
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        results = fn(*args, **given)
+    if here.cuda_stream != stream.cuda_stream:
+        for t in results:
+            if not any(t is x for x in given.values()):
+                t.record_stream(here)
+    return results
+
+
 def _check(status: int, what: str):
     if status != FA_OK:
         raise FAError(status, what)
@@ -390,6 +415,8 @@ def _check(status: int, what: str):
 def attention_fwd(q, k, v, scale: float | None = None, causal: bool = False, out=None, lse=None, stream=None):
     """O, L = attention(q [B,Nq,Hq,d], k/v [B,Nk,Hkv,d]); L is float32 [B,Hq,Nq]."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, q.device, attention_fwd, q, k, v, scale, causal, out=out, lse=lse)
     q, k, v = _dev(q), _dev(k), _dev(v)
     B, Nq, Hq, d = q.shape
     _, Nk, Hkv, _ = k.shape
@@ -398,7 +425,7 @@ def attention_fwd(q, k, v, scale: float | None = None, causal: bool = False, out
     o = torch.empty_like(q) if out is None else out
     L = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
     _check(fa_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), L.data_ptr(), B, Hq, Hkv, Nq, Nk, d,
-                  float(scale), int(bool(causal)), _dtype_code(q), _stream(stream)), "fa_fwd")
+                  float(scale), int(bool(causal)), _dtype_code(q), _stream(None)), "fa_fwd")
     return o, L
 
 
@@ -406,6 +433,9 @@ def attention_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
                          scale: float | None = None, causal: bool = False, out=None, lse=None, stream=None):
     """Packed varlen forward: q [total_q,Hq,d], k/v [total_k,Hkv,d]; L is float32 [Hq,total_q]."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, q.device, attention_varlen_fwd, q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                          max_seqlen_k, scale, causal, out=out, lse=lse)
     q, k, v = _dev(q), _dev(k), _dev(v)
     cu_q = _dev(cu_seqlens_q).to(torch.int32)
     cu_k = _dev(cu_seqlens_k).to(torch.int32)
@@ -417,7 +447,7 @@ def attention_varlen_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
     L = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device) if lse is None else lse
     _check(fa_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), L.data_ptr(), cu_q.data_ptr(),
                          cu_k.data_ptr(), cu_q.numel() - 1, Tq, Tk, int(max_seqlen_q), int(max_seqlen_k), Hq, Hkv,
-                         d, float(scale), int(bool(causal)), _dtype_code(q), _stream(stream)), "fa_varlen_fwd")
+                         d, float(scale), int(bool(causal)), _dtype_code(q), _stream(None)), "fa_varlen_fwd")
     return o, L
 
 
@@ -425,6 +455,8 @@ def attention_bwd(q, k, v, o, lse, dout, scale: float | None = None, causal: boo
                   stream=None):
     """dQ, dK, dV of the fixed-length forward (same layouts as q, k, v)."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, q.device, attention_bwd, q, k, v, o, lse, dout, scale, causal, workspace=workspace)
     q, k, v, o, dout = _dev(q), _dev(k), _dev(v), _dev(o), _dev(dout)
     lse = _dev(lse)
     B, Nq, Hq, d = q.shape
@@ -436,7 +468,7 @@ def attention_bwd(q, k, v, o, lse, dout, scale: float | None = None, causal: boo
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     _check(fa_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                   dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), B, Hq, Hkv, Nq, Nk, d, float(scale),
-                  int(bool(causal)), _dtype_code(q), _stream(stream)), "fa_bwd")
+                  int(bool(causal)), _dtype_code(q), _stream(None)), "fa_bwd")
     return dq, dk, dv
 
 
@@ -444,6 +476,9 @@ def attention_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_
                          scale: float | None = None, causal: bool = False, workspace=None, stream=None):
     """dQ, dK, dV of the packed varlen forward (same layouts as q, k, v; d = 64 or 128)."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, q.device, attention_varlen_bwd, q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k,
+                          max_seqlen_q, max_seqlen_k, scale, causal, workspace=workspace)
     q, k, v, o, dout = _dev(q), _dev(k), _dev(v), _dev(o), _dev(dout)
     lse = _dev(lse)
     cu_q = _dev(cu_seqlens_q).to(torch.int32)
@@ -459,7 +494,7 @@ def attention_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_
     _check(fa_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
                          n, Tq, Tk, int(max_seqlen_q), int(max_seqlen_k), Hq, Hkv, d, float(scale),
-                         int(bool(causal)), _dtype_code(q), _stream(stream)), "fa_varlen_bwd")
+                         int(bool(causal)), _dtype_code(q), _stream(None)), "fa_varlen_bwd")
     return dq, dk, dv
 
 
@@ -472,6 +507,9 @@ def attention_decode(q, k_cache, v_cache, cache_seqlens=None, scale: float | Non
     [num_pages,page_size,Hkv,d] and cache_seqlens required. Returns O [B,Nq,Hq,d]
     and L float32 [B,Hq,Nq]."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, q.device, attention_decode, q, k_cache, v_cache, cache_seqlens, scale, causal,
+                          block_table, workspace=workspace, out=out, lse=lse)
     q, k, v = _dev(q), _dev(k_cache), _dev(v_cache)
     B, Nq, Hq, d = q.shape
     Hkv = k.shape[2]
@@ -485,7 +523,7 @@ def attention_decode(q, k_cache, v_cache, cache_seqlens=None, scale: float | Non
     if block_table is None:
         st = fa_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), L.data_ptr(),
                        0 if sl is None else sl.data_ptr(), ws.data_ptr(), B, Hq, Hkv, Nq, k.shape[1], d, float(scale),
-                       int(bool(causal)), _dtype_code(q), _stream(stream))
+                       int(bool(causal)), _dtype_code(q), _stream(None))
         _check(st, "fa_decode")
     else:
         if sl is None:
@@ -493,7 +531,7 @@ def attention_decode(q, k_cache, v_cache, cache_seqlens=None, scale: float | Non
         bt = _dev(block_table).to(torch.int32)
         st = fa_decode_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), L.data_ptr(), sl.data_ptr(),
                              bt.data_ptr(), ws.data_ptr(), B, Hq, Hkv, Nq, k.shape[0], k.shape[1], bt.shape[1], d,
-                             float(scale), int(bool(causal)), _dtype_code(q), _stream(stream))
+                             float(scale), int(bool(causal)), _dtype_code(q), _stream(None))
         _check(st, "fa_decode_paged")
     return o, L
 
@@ -503,6 +541,9 @@ def attention_fwd_fp8(q8, k8, v8, q_scale, k_scale, v_scale, scale: float | None
     """FP8 forward: q8 [B,Nq,Hq,d], k8/v8 [B,Nk,Hkv,d] uint8 E4M3 codes with float32 block
     factors [B,H,ceil(N/128)]; returns O bf16 [B,Nq,Hq,d] and L float32 [B,Hq,Nq]."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, q8.device, attention_fwd_fp8, q8, k8, v8, q_scale, k_scale, v_scale, scale, causal,
+                          out=out, lse=lse)
     q8, k8, v8 = _dev(q8), _dev(k8), _dev(v8)
     qs, ks, vs = (_dev(t).to(torch.float32) for t in (q_scale, k_scale, v_scale))
     B, Nq, Hq, d = q8.shape
@@ -513,7 +554,7 @@ def attention_fwd_fp8(q8, k8, v8, q_scale, k_scale, v_scale, scale: float | None
     L = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q8.device) if lse is None else lse
     _check(fa_fwd_fp8(q8.data_ptr(), k8.data_ptr(), v8.data_ptr(), qs.data_ptr(), ks.data_ptr(), vs.data_ptr(),
                       o.data_ptr(), L.data_ptr(), B, Hq, Hkv, Nq, Nk, d, float(scale), int(bool(causal)),
-                      _stream(stream)), "fa_fwd_fp8")
+                      _stream(None)), "fa_fwd_fp8")
     return o, L
 
 
@@ -564,17 +605,6 @@ def _call(index: int, stream, what: str, fn, *args):
             st = fn(*args, _stream(stream))
     if st != FA_OK:
         raise FAError(st, what)
-
-
-def _temporary(t, stream):
-    """A buffer of this call alone, kept from other uses until `stream` has run the call."""
-    if stream is not None:
-        T = _torch()
-        if not hasattr(stream, "cuda_stream"):
-            stream = T.cuda.ExternalStream(int(stream), device=t.device) if int(stream) else \
-                T.cuda.default_stream(t.device)
-        t.record_stream(stream)
-    return t
 
 
 _Pair = ctypes.c_longlong * 2
@@ -628,6 +658,9 @@ def attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens=No
     [B,max_pages]): k/v [num_pages,page_size,Hkv,d], k/v_scale [num_pages,Hkv], cache_seqlens
     required. `workspace`: uint8, fa_decode_fp8_workspace_size(B,Hq,Hkv,Nq,d) bytes (one is made
     when None). Returns O [B,Nq,Hq,d] (q's type) and L float32 [B,Hq,Nq]."""
+    if stream is not None:
+        return _on_stream(stream, q.device, attention_decode_fp8, q, k_cache, v_cache, k_scale, v_scale, cache_seqlens,
+                          scale, causal, block_table, workspace=workspace, out=out, lse=lse)
     T = _torch()
     f32, i32, dt = T.float32, T.int32, q.dtype
     index = q.get_device()
@@ -643,7 +676,7 @@ def attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens=No
     if lse is None:
         lse = T.empty((B, Hq, Nq), dtype=f32, device=q.device)
     if workspace is None:
-        workspace = _temporary(T.empty(need, dtype=T.uint8, device=q.device), stream)
+        workspace = T.empty(need, dtype=T.uint8, device=q.device)
     if not ((dt is T.bfloat16 or dt is T.float16) and index >= 0 and q.is_contiguous()
             and kshape == (n0 if paged else B, n1, Hkv, d) and v_cache.shape == kshape
             and (k_cache.dtype is T.uint8 or k_cache.dtype is T.float8_e4m3fn) and k_cache.is_contiguous()
@@ -677,12 +710,12 @@ def attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens=No
     sl = None if cache_seqlens is None else cache_seqlens.data_ptr()
     code = FA_BF16 if dt is T.bfloat16 else FA_FP16
     if paged:
-        _call(index, stream, "fa_decode_paged_fp8", lib().fa_decode_paged_fp8, q.data_ptr(), k_cache.data_ptr(),
+        _call(index, None, "fa_decode_paged_fp8", lib().fa_decode_paged_fp8, q.data_ptr(), k_cache.data_ptr(),
               v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), lse.data_ptr(), sl,
               block_table.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nq, n0, n1, block_table.shape[1], d, scale,
               bool(causal), code)
     else:
-        _call(index, stream, "fa_decode_fp8", lib().fa_decode_fp8, q.data_ptr(), k_cache.data_ptr(),
+        _call(index, None, "fa_decode_fp8", lib().fa_decode_fp8, q.data_ptr(), k_cache.data_ptr(),
               v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), lse.data_ptr(), sl,
               workspace.data_ptr(), B, Hq, Hkv, Nq, n1, d, scale, bool(causal), code)
     return out, lse
@@ -696,6 +729,10 @@ def build_block_tables(cache_seqlens, new_lens, free_pages, block_table, page_si
     [num_free]. Returns slot_map int32 [total_new] (page * page_size + row of every packed new
     token, -1 for none), cu_new int32 [B+1], new_seqlens int32 [B] and pages_used int32 [1], the
     number of entries of free_pages taken."""
+    if stream is not None:
+        return _on_stream(stream, new_lens.device, build_block_tables, cache_seqlens, new_lens, free_pages, block_table,
+                          page_size, num_pages, total_new, slot_map=slot_map, cu_new=cu_new, new_seqlens=new_seqlens,
+                          pages_used=pages_used)
     T = _torch()
     i32, index = T.int32, new_lens.get_device()
     B, pages, num_free = new_lens.shape[0], block_table.shape[-1], free_pages.numel()
@@ -713,7 +750,7 @@ def build_block_tables(cache_seqlens, new_lens, free_pages, block_table, page_si
         _need(new_seqlens, "new_seqlens", i32, index, (B,))
     pages_used = T.empty(1, dtype=i32, device=dev) if pages_used is None else \
         _need(pages_used, "pages_used", i32, index, (1,))
-    _call(index, stream, "fa_build_block_tables", lib().fa_build_block_tables,
+    _call(index, None, "fa_build_block_tables", lib().fa_build_block_tables,
           None if cache_seqlens is None else cache_seqlens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
           block_table.data_ptr(), slot_map.data_ptr(), cu_new.data_ptr(), new_seqlens.data_ptr(),
           pages_used.data_ptr(), B, num_free, num_pages, page_size, pages, total_new)
