@@ -467,7 +467,11 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 tmem_ld32(s_addr + 64 * half + 32, sv[1]);
                 const float4 f4 = *reinterpret_cast<const float4*>(s_sc);
                 const float4 v4 = *reinterpret_cast<const float4*>(s_sc + 8);
-                const float kf[4] = {f4.x * my_qf, f4.y * my_qf, f4.z * my_qf, f4.w * my_qf};
+                // Masked scores are -inf before they are scaled and have to stay so: a product below
+                // fp32's range (a zero row over a block of zeros: 2^-200) counts as the smallest
+                // normal value instead, with which any raw score is below 2^-100.
+                auto scaled = [my_qf](float f) { return f * my_qf == 0.f ? 1.17549435e-38f : f * my_qf; };
+                const float kf[4] = {scaled(f4.x), scaled(f4.y), scaled(f4.z), scaled(f4.w)};
                 tmem_ld_wait(sv[0]);
                 tmem_ld_wait(sv[1]);
                 if (__any_sync(0xffffffffu, lim < 64)) {
