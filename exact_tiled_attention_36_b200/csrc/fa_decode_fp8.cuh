@@ -16,13 +16,16 @@
 // Products, with keys along the tensor core's M = 128 as in the 16-bit narrow kernel:
 //     S^T = K8 Q^T      (M = 128 keys, N = rows x terms, K = d)
 //     O_t^T = V8^T P^T  (M = d,        N = rows x terms, K = 128 keys)
-// Unlike there, P of a tile is taken relative to the TILE's largest score, and O_t is a
-// product of its own, added to the running output in registers with the factor
+// Unlike there, P of a tile carries its block's V factor and is taken relative to the row's
+// largest such product in the TILE: with u_j = v_f(j) / v_max(tile),
+//     w_j = 2^(s_j + log2 u_j - m_tile),   m_tile = max over the row's keys of s_j + log2 u_j,
+// and O_t = V8^T w is a product of its own, added to the running output in registers with
 //     f = 2^(m_tile - m_run) v_max(tile) / 256
-// per row: E4M3 spans 2^17, and with a reference that stays at the running maximum the
-// small weights of a long tail behind one large key would all round to zero. This also
-// frees the accumulation from rescaling in TMEM, and block factors of V of any size
-// enter f (the tile's largest) and P (a block's share of it).
+// per row; the sum of weights takes w_j / u_j. E4M3 spans 2^17: with a reference that stays
+// at the running maximum the small weights of a long tail behind one large key would all
+// round to zero, and so would those beside a block with a large factor to which the row gives
+// no weight (or that it must not see), were the factor taken into account after the maximum.
+// It also frees the accumulation from rescaling in TMEM. u_j counts as at least 2^-64.
 //
 // Work split: an item is (sequence, KV head, chunk of RC query rows); d = 64: two adjacent
 // KV heads, whose code rows form one 128-byte row (S^T of each is a product over its own 64
@@ -98,8 +101,9 @@ struct Dec8Cfg {
     static constexpr int kBarOff = kRingOff + kUnits * kTile;
     static constexpr int kNumBars = 2 * kUnits + 2 * kQB + 2 * kScSlots + 8 + 3 * NW + 2 * kNotices;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 224 bytes: dec8_locate
-    static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][40]
-    static constexpr int kQfOff = kScOff + kScSlots * 40 * 4;     // float [2][RT]: scale of a query row
+    static constexpr int kScOff = (kMiscOff + 224 + 15) / 16 * 16;  // float [slots][kScSlot]
+    static constexpr int kScSlot = 52;
+    static constexpr int kQfOff = kScOff + kScSlots * kScSlot * 4;  // float [2][RT]: scale of a query row
     // A warpgroup's share of each: its RW rows.
     static constexpr int kRedOff = kQfOff + 2 * RT * 4;           // float [NW][2][4][RW]: warps' maxima
     static constexpr int kRowOff = kRedOff + 8 * RT * 4;          // float [NW][4][5][RW]: a warp's row values
@@ -436,6 +440,21 @@ __device__ __forceinline__ void dec8_hide_nan(uint8_t* tile, int key0, int first
     }
 }
 
+// A block's V factor as a share of a reference 2^ref: its log2 (which joins the scores) and its
+// inverse (which takes it out of their sum). Shares below 2^-64 (also 0, of a page outside the pool,
+// whose codes are zeros) count as 2^-64, so that a sum of inverses stays in fp32's range; NaN stays.
+// Exact for powers of two. (With divisions and log2f, which are code of their own, the loops waited for
+// instructions: ragged pages 50.5 us against 45.7, 128 rows of a head 165 against 148.)
+__device__ __forceinline__ float lg2_approx(float x) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float dec8_share(float v, float ref) {
+    const float lg = lg2_approx(v) - ref;
+    return lg < -64.f ? -64.f : lg;
+}
+
 // ------------------------------------------------------------------- split kernel
 template <bool BF16, bool PAIR, bool PAGED, int RT>
 __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
@@ -660,7 +679,8 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
     } else if (warp == 2) {
         // ------------------------------------------------------------ block factors
         // Lane x + 8 kv + 16 h: box x of a tile, key or value factor, head h of the pair. A
-        // slot holds 16 key factors [h][box], 16 value shares 256 v / v_max and v_max / 256 [h].
+        // slot holds, [h][box], 16 key factors, log2 of 16 value shares u = v / v_max and 16 inverses
+        // 1 / (256 u), and v_max / 256 [h].
         const int x = lane & 7, kv = (lane >> 3) & 1, h = lane >> 4;
         const int pb = args.page_box;
         int gk = 0;
@@ -689,9 +709,11 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
 #pragma unroll
                 for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                 if (!(ok = warp_all(mbar_wait(&sc_empty[slot], ((gg / SC) & 1) ^ 1u, wc, 126)))) break;
-                float* s = sc + slot * 40;
-                s[kv * 16 + h * 8 + x] = kv && top > 0.f ? v / top * 256.f : v;  // (top 0: v is 0, or NaN to be seen)
-                if (kv == 1 && x == 0) s[32 + h] = top * (1.f / 256.f);
+                float* s = sc + slot * C::kScSlot;
+                const float lg = dec8_share(v, top > 0.f ? lg2_approx(top) : 0.f);
+                s[kv * 16 + h * 8 + x] = kv ? lg : v;
+                if (kv) s[32 + h * 8 + x] = ex2_approx(-8.f - lg);
+                if (kv && x == 0) s[48 + h] = top * (1.f / 256.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc_full[slot]);
                 v = next;
@@ -831,10 +853,11 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 const int gg = gk + j, par = gg & 1, slot = gg % SC;
                 ok = warp_all(mbar_wait(&sc_full[slot], (gg / SC) & 1, wc, 130));
                 if (!ok) break;
-                const float* s_sc = sc + slot * 40;
+                const float* s_sc = sc + slot * C::kScSlot;
                 const float kf0 = s_sc[8 * wg_hd + box], kf1 = kMixed ? s_sc[8 + box] : 0.f;
-                const float vs0 = s_sc[16 + 8 * wg_hd + box], vs1 = kMixed ? s_sc[24 + box] : 0.f;
-                const float my_vm = s_sc[32 + my_hd];
+                const float vl0 = s_sc[16 + 8 * wg_hd + box], vl1 = kMixed ? s_sc[24 + box] : 0.f;
+                const float vi0 = s_sc[32 + 8 * wg_hd + box], vi1 = kMixed ? s_sc[40 + box] : 0.f;
+                const float my_vm = s_sc[48 + my_hd];
                 ok = warp_all(mbar_wait(&s_full[par], (gg >> 1) & 1, wc, 131));
                 if (!ok) break;
                 __syncwarp();
@@ -862,11 +885,11 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                             auto two = [&](int t) {
                                 return f2_pack(__uint_as_float(s[t][r + i]), __uint_as_float(s[t][r + i + 1]));
                             };
-                            const float kf = kMixed && r + i >= RH ? kf1 : kf0;
+                            const float kf = kMixed && r + i >= RH ? kf1 : kf0, vl = kMixed && r + i >= RH ? vl1 : vl0;
                             uint64_t v = two(NT - 1);
 #pragma unroll
                             for (int t = NT - 2; t >= 0; --t) v = f2_fma(v, f2_pack(0.0625f, 0.0625f), two(t));
-                            f2_unpack(f2_mul(f2_mul(v, f2_pack(f[i], f[i + 1])), f2_pack(kf, kf)), x[r + i], x[r + i + 1]);
+                            f2_unpack(f2_fma(f2_mul(v, f2_pack(f[i], f[i + 1])), f2_pack(kf, kf), f2_pack(vl, vl)), x[r + i], x[r + i + 1]);
                         }
                     }
                 }
@@ -880,7 +903,8 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                     for (int r = 0; r < RW; ++r)
                         if (key >= row_hi[r]) x[r] = -INFINITY;
                 }
-                // Every row's largest score of the tile: over the warp, then the four warps.
+                // Every row's largest product of weight and V factor in the tile (log2): over the warp,
+                // then the four warps.
                 float* rd = red + par * 4 * RW;
 #pragma unroll
                 for (int r = 0; r < RW; r += 4) {
@@ -901,13 +925,13 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                     }
                     const bool none = mt == -INFINITY;
                     const float f = none ? 0.f : ex2_approx(mt - m_run);
-                    row_m[lane] = none ? 0.f : -mt;
+                    row_m[lane] = none ? 0.f : 8.f - mt;
                     row_f[par * RW + lane] = f;
                     row_a[lane] = alpha;
                 }
                 moved = __any_sync(0xffffffffu, moved);
                 __syncwarp();
-                // P = 2^(x - m_tile), its sum in the running scale, and its terms times V's share.
+                // w = 256 2^(x - m_tile), the weights' sum in the running scale, and the terms of w.
                 // Row n, key l in the unswizzled layout: rows at constant offsets from the key's place
                 // (the 128-byte swizzle would cost an address of its own for every row).
                 uint8_t* pb = sP + par * C::N * 128 + (first >> 3) * 1024 + (first & 7) * 16 + (l_idx >> 4) * 128 + (l_idx & 15);
@@ -925,11 +949,11 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
                         const float p0 = ex2_approx(x[r + i] + mm[i]), p1 = ex2_approx(x[r + i + 1] + mm[i + 1]);
-                        l[r + i] = fmaf(p0, ff[i], l[r + i]);
-                        l[r + i + 1] = fmaf(p1, ff[i + 1], l[r + i + 1]);
+                        const float vi = kMixed && r + i >= RH ? vi1 : vi0;  // (pairs of rows are of one head)
+                        l[r + i] = fmaf(p0 * vi, ff[i], l[r + i]);
+                        l[r + i + 1] = fmaf(p1 * vi, ff[i + 1], l[r + i + 1]);
                         uint32_t c[NT];
-                        e4m3_terms<NT>(pack2<false>(p0 * (kMixed && r + i >= RH ? vs1 : vs0),
-                                                    p1 * (kMixed && r + i + 1 >= RH ? vs1 : vs0)), c);
+                        e4m3_terms<NT>(pack2<false>(p0, p1), c);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             const int n0 = t * RT + r + i, n1 = n0 + 1;  // past the warpgroup's first row

@@ -12,9 +12,12 @@
 // into the same columns (unscaled terms: exact where a value is within 2^-10 of the row's
 // largest, else to 2^-18 of that). P needs a wide exponent range, which E4M3 terms do not
 // have when a row keeps one reference: it is rounded to fp16, and four warps expand V's codes
-// to fp16 in shared memory (exact). The keys' block factors join each score, the values'
-// factors P, as their share of the largest one met so far (O is in units of that one and
-// rescaled when it grows).
+// to fp16 in shared memory (exact). The keys' block factors join each score, and so does log2 of
+// the values', as their share u of a power of two v_ref near the largest one met so far:
+//     w = 2^(s + log2 u - m),   m at most 8 below the row's largest s + log2 u so far,
+// so a block to which the row gives no weight, or that it must not see, costs the other weights
+// nothing, whatever its factor. The sum of weights takes w / u; O is in units of v_ref 2^m, and
+// when v_ref grows, m falls by as much and the products stay as they are. u counts as at least 2^-64.
 //
 // Work split, segments, teams and merge: fa_decode_fp8.cuh, with one item per KV head. For
 // d = 64 a tile still loads the 128 bytes of two heads (the neighbouring CTA of the team
@@ -49,10 +52,11 @@ struct Dec8RowsCfg {
     static constexpr int kVOff = kQOff + NT * kRaw;
     static constexpr int kRawOff = kVOff + 2 * kTile;
     static constexpr int kBarOff = kRawOff + kUnits * kRaw;
-    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 12 + 2 * kNotices;
+    static constexpr int kNumBars = 2 * kUnits + 4 + 2 + 2 * kScSlots + 4 + 3 + 2 + 16 + 2 * kNotices;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // 288 bytes: dec8_locate
-    static constexpr int kScOff = (kMiscOff + 288 + 15) / 16 * 16;  // float [slots][20]
-    static constexpr int kQfOff = kScOff + kScSlots * 20 * 4;     // float [128]: scale of a query row
+    static constexpr int kScOff = (kMiscOff + 288 + 15) / 16 * 16;  // float [slots][kScSlot]
+    static constexpr int kScSlot = 28;
+    static constexpr int kQfOff = kScOff + kScSlots * kScSlot * 4;     // float [128]: scale of a query row
     static constexpr int kExOff = kQfOff + 128 * 4;               // float [3][2][128]: a row's halves (two tiles' maxima, sums)
     static constexpr int kLenOff = kExOff + 6 * 128 * 4;          // int [256]
     static constexpr int kLens = 256;
@@ -94,8 +98,8 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
     uint64_t* o_free = o_ready + 1;    // O has been read
     uint64_t* mma_done = o_free + 1;
     uint64_t* sm_done = mma_done + 1;
-    uint64_t* pair = sm_done + 1;      // [4][3] the two warps of 32 rows: per tile parity, per segment
-    uint64_t* v_seen = pair + 12;      // [kNotices] a tile's values looked through by dec8_hide_nan
+    uint64_t* pair = sm_done + 1;      // [4][4] the two warps of 32 rows: per tile parity, per segment, per step of v_ref
+    uint64_t* v_seen = pair + 16;      // [kNotices] a tile's values looked through by dec8_hide_nan
     uint64_t* v_due = v_seen + kNotices;  // [kNotices] the load of such a tile has begun
     float* sc = reinterpret_cast<float*>(smem + C::kScOff);
     float* qf = reinterpret_cast<float*>(smem + C::kQfOff);
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
         }
         mbar_init(mma_done, 1);
         mbar_init(sm_done, n_act);
-        for (int i = 0; i < 12; ++i) mbar_init(&pair[i], 2);
+        for (int i = 0; i < 16; ++i) mbar_init(&pair[i], 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -283,7 +287,8 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
     } else if (warp == 2) {
         // ------------------------------------------------------------ block factors
         // Lane x + 8 kv: keys 16 x .. of a tile, key or value factor. A slot holds the 8 key
-        // factors, the 8 value factors as shares of the tile's largest, and that.
+        // factors, log2 and inverse of the 8 value factors as shares of v_ref, that power of two (the
+        // segment's largest factor so far, rounded down; 0: none yet) and log2 of its step.
         const int x = lane & 7, kv = (lane >> 3) & 1;
         int gk = 0;
         bool ok = true;
@@ -301,19 +306,28 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                     return f[(static_cast<size_t>(it.b) * args.Hkv + it.hh) * args.per_seq + kt];
                 }
             };
-            float v = read(j0);
+            float v = read(j0), v_ref = 0.f, e_ref = 0.f;  // v_ref = 2^e_ref, or 0
             for (int j = 0; j < n; ++j) {
                 const int gg = gk + j, slot = gg % SC;
                 const float next = j + 1 < n ? read(j0 + j + 1) : 0.f;
-                float top = v;
+                float top = v, step = 0.f;
 #pragma unroll
                 for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                top = __shfl_sync(0xffffffffu, top, 8);
+                const int e = max(static_cast<int>(__float_as_uint(top) >> 23), 1) - 127;
+                if (top > 0.f && (v_ref == 0.f || static_cast<float>(e) > e_ref)) {
+                    if (v_ref > 0.f) step = static_cast<float>(e) - e_ref;
+                    v_ref = exp2_int(e);
+                    e_ref = static_cast<float>(e);
+                }
+                const float lg = dec8_share(v, e_ref);
                 if (!(ok = warp_all(mbar_wait(&sc_empty[slot], ((gg / SC) & 1) ^ 1u, wc, 147)))) break;
-                float* s = sc + slot * 20;
+                float* s = sc + slot * C::kScSlot;
                 // Keys without a block (past the end, pages outside the pool) have zero codes or
                 // are masked: any key factor does, but -inf times it has to stay -inf.
-                if (lane < 16) s[kv * 8 + x] = kv ? (top > 0.f ? v / top : v) : (v == 0.f ? 1.f : v);
-                if (lane == 8) s[16] = top;
+                if (lane < 16) s[kv * 8 + x] = kv ? lg : (v == 0.f ? 1.f : v);
+                if (lane < 16 && kv) s[16 + x] = ex2_approx(-lg);
+                if (lane == 8) *reinterpret_cast<float2*>(s + 24) = make_float2(v_ref, step);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc_full[slot]);
                 v = next;
@@ -431,13 +445,13 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
         const uint32_t o_addr = lane_base + C::kColO + half * (D / 2);  // this thread's outputs
         float* ex = reinterpret_cast<float*>(smem + C::kExOff);
-        uint64_t* meets = pair + 3 * w4;
+        uint64_t* meets = pair + 4 * w4;
         auto meet = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
             return warp_all(mbar_wait(bar, parity, wc, site));
         };
-        int gk = 0, nq = 0;
+        int gk = 0, nq = 0, n_steps = 0;
         bool ok = true;
         for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
             int j0, n;
@@ -455,8 +469,9 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 const int gg = gk + j, b = gg & 1, slot = gg % SC;
                 ok = warp_all(mbar_wait(&sc_full[slot], (gg / SC) & 1, wc, 153));
                 if (!ok) break;
-                const float* s_sc = sc + slot * 20 + 4 * half;
-                const float top = sc[slot * 20 + 16];
+                const float* s_sc = sc + slot * C::kScSlot + 4 * half;
+                const float2 ref = *reinterpret_cast<const float2*>(sc + slot * C::kScSlot + 24);
+                v_ref = ref.x;
                 ok = warp_all(mbar_wait(&s_full[b], (gg >> 1) & 1, wc, 154));
                 if (!ok) break;
                 tc_fence_after();
@@ -466,12 +481,30 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 tmem_ld32(s_addr + 64 * half, sv[0]);
                 tmem_ld32(s_addr + 64 * half + 32, sv[1]);
                 const float4 f4 = *reinterpret_cast<const float4*>(s_sc);
-                const float4 v4 = *reinterpret_cast<const float4*>(s_sc + 8);
+                const float4 g4 = *reinterpret_cast<const float4*>(s_sc + 8);
+                const float vl[4] = {g4.x, g4.y, g4.z, g4.w};
                 // Masked scores are -inf before they are scaled and have to stay so: a product below
                 // fp32's range (a zero row over a block of zeros: 2^-200) counts as the smallest
                 // normal value instead, with which any raw score is below 2^-100.
                 auto scaled = [my_qf](float f) { return f * my_qf == 0.f ? 1.17549435e-38f : f * my_qf; };
                 const float kf[4] = {scaled(f4.x), scaled(f4.y), scaled(f4.z), scaled(f4.w)};
+                float alpha = 1.f;
+                bool resc = false;
+                if (ref.y > 0.f) {
+                    // v_ref 2^step: m falls by the step, O stays, the sum of weights 2^(s - m) grows. Past
+                    // 2^80 of that sum (of both halves) O is scaled down instead: 2^72 a key still to come
+                    // leaves fp32's range to more keys than a sequence has.
+                    ex[(4 + half) * 128 + r] = l;
+                    ok = meet(&meets[3], n_steps++ & 1, 162);
+                    if (!ok) break;
+                    const float both = l + ex[(5 - half) * 128 + r];
+                    const int room = min(max(80 - (static_cast<int>(__float_as_uint(both) >> 23) - 127), 0), 120);
+                    const float down = fminf(ref.y, static_cast<float>(room));
+                    m -= down;
+                    l *= exp2_int(static_cast<int>(down));
+                    alpha = ex2_approx(down - ref.y);
+                    resc = down < ref.y;
+                }
                 tmem_ld_wait(sv[0]);
                 tmem_ld_wait(sv[1]);
                 if (__any_sync(0xffffffffu, lim < 64)) {
@@ -479,7 +512,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                     for (int i = 0; i < 64; ++i)
                         if (i >= lim) sv[i >> 5][i & 31] = __float_as_uint(-INFINITY);
                 }
-                // The largest scaled score: a block's largest raw one is scaled.
+                // The largest scaled score with its V share: a block's largest raw one is scaled.
                 float mx = -INFINITY;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -488,7 +521,7 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                     for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(sv[g >> 1][16 * (g & 1) + i]);
                     const float a = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
                     const float c = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
-                    mx = fmaxf(mx, fmaxf(a, c) * kf[g]);
+                    mx = fmaxf(mx, fmaf(fmaxf(a, c), kf[g], vl[g]));
                 }
                 // The row's other half (and both have read the scores' columns from here on).
                 tc_fence_before();
@@ -497,46 +530,37 @@ __global__ void __launch_bounds__(Dec8RowsCfg<BF16, D>::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 mx = fmaxf(mx, ex[(b * 2 + 1 - half) * 128 + r]);
-                float alpha = 1.f;
-                bool resc = false;
                 if (mx > m + kRescaleThreshold) {
                     if (m != -INFINITY) {
-                        alpha = ex2_approx(m - mx);
+                        const float a = ex2_approx(m - mx);
+                        alpha *= a;
+                        l *= a;
                         resc = true;
                     }
                     m = mx;
                 }
-                l *= alpha;
-                // O counts in units of the largest V factor met so far.
-                if (top > v_ref) {
-                    if (v_ref > 0.f) {
-                        alpha *= v_ref / top;
-                        resc = true;
-                    }
-                    v_ref = top;
-                }
-                const float share = v_ref > 0.f ? __fdividef(top, v_ref) : 0.f;
                 const float neg_m = m == -INFINITY ? 0.f : -m;
-                const uint64_t m2 = f2_pack(neg_m, neg_m);
-                const float vs[4] = {v4.x * share, v4.y * share, v4.z * share, v4.w * share};
-                uint64_t sums[2] = {0, 0};
                 uint32_t pk[16];
+                // (The shares once more: kept over the maximum they cost registers, 126 against 117 us.)
+                const float4 h4 = *reinterpret_cast<const float4*>(s_sc + 8);
+                const float4 i4 = *reinterpret_cast<const float4*>(s_sc + 16);
+                const float vm[4] = {h4.x + neg_m, h4.y + neg_m, h4.z + neg_m, h4.w + neg_m}, vi[4] = {i4.x, i4.y, i4.z, i4.w};
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint64_t c2 = f2_pack(kf[g], kf[g]), w2 = f2_pack(vs[g], vs[g]);
+                    const uint64_t c2 = f2_pack(kf[g], kf[g]), m2 = f2_pack(vm[g], vm[g]);
+                    uint64_t sum = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int k = 16 * (g & 1) + 2 * i;
-                        float y0, y1, z0, z1;
+                        float y0, y1;
                         f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[g >> 1][k]), __uint_as_float(sv[g >> 1][k + 1])), c2, m2), y0, y1);
-                        const uint64_t p2 = f2_pack(ex2_approx(y0), ex2_approx(y1));
-                        sums[g & 1] = f2_add(sums[g & 1], p2);
-                        f2_unpack(f2_mul(p2, w2), z0, z1);
-                        pk[8 * (g & 1) + i] = pack2<false>(z0, z1);
+                        const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+                        sum = f2_add(sum, f2_pack(p0, p1));
+                        pk[8 * (g & 1) + i] = pack2<false>(p0, p1);
                     }
+                    l = fmaf(f2_sum(sum), vi[g], l);
                     if (g & 1) tmem_st16(s_addr + 32 * half + 8 * (g - 1), pk);
                 }
-                l += f2_sum(f2_add(sums[0], sums[1]));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc_empty[slot]);
                 // Rescale O once the previous tile's P V is complete.

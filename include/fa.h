@@ -437,8 +437,13 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
  *     K[j, h, :] = k_scale(block of j, h) * e4m3(k[j, h, :]), and likewise V,
  * so a cache takes half the bytes of a 16-bit one. The queries keep their 16 bits: each
  * row is scaled by a power of two and taken exactly where a value is within 2^-10 of the
- * row's largest, else to 2^-18 of that. P is rounded to 8 significant bits for bf16 and 11
- * for fp16 (at least; weights below 2^-17 of a tile's largest, to 2^-22 of it). Sums are fp32.
+ * row's largest, else to 2^-18 of that. Each weight times its block's V factor is rounded to
+ * 8 significant bits for bf16 and 11 for fp16 at least; products below 2^-17 of the row's
+ * largest in the same 128 keys are rounded to 2^-22 of that one (with more than 32 query rows
+ * a KV head, d = 64: 24, those below 2^-14 of the row's largest so far to 2^-24 of it). Keys
+ * the row does not see, and blocks it gives no weight to, have no part in these bounds,
+ * whatever their factors, but for one: a V factor counts as at least 2^-64 of the largest
+ * among the same 128 keys (many rows: of the largest so far). Sums are fp32.
  *   q [B,Nq,Hq,d] and o (dtype), lse [B,Hq,Nq] (float32): as fa_decode.
  *   fa_decode_fp8: k, v [B,Nk,Hkv,d] E4M3 bytes; a block is 128 tokens: k_scale, v_scale
  *       DEVICE float32 [B,Hkv,ceil(Nk/128)] (the layout of fa_fwd_fp8).
