@@ -722,13 +722,18 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ query terms, NaN of new tokens
-        int gk = 0, nq = 0, n_told = 0;
-        bool ok = true;
-        for (Dec8Item it = rg.first; ok && it.P < rg.hi; it = dec8_next(args, rg, it)) {
-            int j0, n;
-            if (!dec8_segment(rg, it, j0, n)) continue;
-            const int qb = nq % QB;
-            if (nq > 0) {  // the first segment's: the softmax warps
+        // The next segment's queries first, then NaN in the segment before: its last tiles may still
+        // be on their way, and the next products would wait for their queries meanwhile.
+        int gk = 0, n_told = 0;
+        int p_len = 0, p_j0 = 0, p_n = 0;  // the segment before
+        bool ok = true, more = true;
+        Dec8Item it = rg.first;
+        for (int nq = 0; ok && more; ++nq) {
+            int j0 = 0, n = 0;
+            while (it.P < rg.hi && !dec8_segment(rg, it, j0, n)) it = dec8_next(args, rg, it);
+            more = it.P < rg.hi;
+            if (more && nq > 0) {  // the first segment's: the softmax warps
+                const int qb = nq % QB;
                 uint4 raw = dec8_query_load<C, PAIR, RT>(args, it, lane);
                 if (!(ok = warp_all(mbar_wait(&q_empty[qb], ((nq / QB) & 1) ^ 1u, wc, 127)))) break;
 #pragma unroll 1
@@ -741,17 +746,17 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[qb]);
             }
-            const int first_part = it.len - args.Nq + 1;
-            if (part_seen && (j0 + n) * 128 > first_part) {
-                // Segment nq - 3, the last to use this part of the notes, has been read: the queries'
-                // buffer of segment nq - 2 came free after it.
-                uint32_t* noted = reinterpret_cast<uint32_t*>(smem + C::kNanOff + nq % 3 * 128) + lane;
+            const int first_part = p_len - args.Nq + 1;
+            if (nq > 0 && part_seen && (p_j0 + p_n) * 128 > first_part) {
+                // Segment nq - 4, the last to use this part of the notes, has been read: the queries'
+                // buffer of segment nq - 3 came free after it.
+                uint32_t* noted = reinterpret_cast<uint32_t*>(smem + C::kNanOff + (nq - 1) % 3 * 128) + lane;
                 uint32_t first = 0xffffffffu;
-                for (int j = max(first_part / 128 - j0, 0); j < n; ++j) {
-                    const int key0 = (j0 + j) * 128, uv = 2 * (gk + j) + 1;
+                for (int j = max(first_part / 128 - p_j0, 0); j < p_n; ++j) {
+                    const int key0 = (p_j0 + j) * 128, uv = 2 * (gk + j) + 1;
                     if (!(ok = warp_all(mbar_wait(&v_due[notice_bar(n_told)], notice_parity(n_told), wc, 137)))) break;
                     if (!(ok = warp_all(mbar_wait(&full[uv % U], (uv / U) & 1, wc, 136)))) break;
-                    dec8_hide_nan(ring + (uv % U) * C::kTile, key0, first_part, it.len, first);
+                    dec8_hide_nan(ring + (uv % U) * C::kTile, key0, first_part, p_len, first);
                     *noted = first;
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -759,8 +764,11 @@ __global__ void __launch_bounds__(Dec8Cfg<BF16, PAIR, RT>::kThreads, kDec8Ctas)
                     ++n_told;
                 }
             }
-            gk += n;
-            ++nq;
+            gk += p_n;
+            p_len = it.len;
+            p_j0 = j0;
+            p_n = n;
+            if (more) it = dec8_next(args, rg, it);
         }
     } else {
         // ------------------------------------------------------------ softmax, output
