@@ -8,10 +8,12 @@ and the block tables), side by side, and links them into
 exact_tiled_attention_36_b200/libfa.so, with the CUDA runtime linked
 statically so the library loads on a machine without a GPU driver (the
 driver is reached at run time through the runtime's entry-point query). An object
-whose source and headers did not change since it was built is used again.
+whose source and headers did not change since it was built, by the same compiler and
+flags, is used again, and so is the library; `extra` flags give objects of their own.
 """
 from __future__ import annotations
 
+import hashlib
 import os
 import subprocess
 import sys
@@ -33,6 +35,19 @@ FLAGS = [
 ]
 
 
+def _key(extra: list[str] | None) -> str:
+    """Of the compiler and its flags: part of an object's name, and noted beside the library it went into."""
+    return hashlib.sha256("\0".join([NVCC, *FLAGS, *(extra or [])]).encode()).hexdigest()[:12]
+
+
+def _other_flags(key: str) -> bool:
+    """Whether the library is noted to have been linked from objects of another key."""
+    try:
+        return open(os.path.join(OBJ_DIR, "linked")).read() != key
+    except OSError:
+        return False
+
+
 def _fresh(obj: str) -> bool:
     """Whether `obj` is newer than every file its header list (make syntax) names, and this script."""
     try:
@@ -45,13 +60,14 @@ def _fresh(obj: str) -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     newest = max(os.path.getmtime(p) for p in DEPS)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest and not extra:
+    key = _key(extra)
+    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest and not extra and not _other_flags(key):
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc")]
     objs, running = [], []
     for src in SRCS:
-        obj = os.path.join(OBJ_DIR, os.path.basename(src)[:-3] + ".o")
+        obj = os.path.join(OBJ_DIR, f"{os.path.basename(src)[:-3]}.{key}.o")
         objs.append(obj)
         if not force and not extra and _fresh(obj):
             continue
@@ -74,6 +90,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
+    with open(os.path.join(OBJ_DIR, "linked"), "w") as f:
+        f.write(key)
     os.replace(tmp, LIB)
     return LIB
 
