@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(TG == 32 ? 256 : TG, TG == 32 ? 4 : 1024 / TG)
         const int pg = a.block_table[static_cast<size_t>(b) * a.per_seq + blk];
         if (pg < 0 || pg >= a.num_pages) {
             if (h == 0 && kv == 0 && tg == 0) atomicCAS(a.err, 0, kErrCacheRange);
+            asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives its CTA's shared memory
             return;
         }
         dst = a.codes[kv] + static_cast<size_t>(pg) * a.unit * per_row + h * D;
