@@ -48,6 +48,7 @@
 
 #include "fa_cache.cuh"
 #include "notice_ring.h"
+#include "segment_range.h"
 #include "sm100.cuh"
 
 namespace fa {
@@ -1081,9 +1082,9 @@ __global__ void __launch_bounds__(WIDE ? 32 * kDec8WideWarps : 128) fa_decode8_c
     // from here on.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int2 cc = a.meta[item];  // of an item without keys: anything
-    const int len = dec8_len(a, b);
-    const int c0 = len > 0 ? cc.x : 0, c1 = len > 0 ? cc.y : -1;
+    const int2 cc = a.meta[item];
+    const SegmentRange seg = segment_range(cc.x, cc.y, dec8_len(a, b), a.teams);
+    const int c0 = seg.first, c1 = seg.last;
     // The segment of team c lies c TS RT rows further.
     const size_t s0 = dec8_slot(a, 0, b, vh / a.TS, vh % a.TS) * a.RT + r, step = static_cast<size_t>(a.TS) * a.RT;
     const float* lp = a.lse_part + s0;
