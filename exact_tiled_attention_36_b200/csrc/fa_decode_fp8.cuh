@@ -424,10 +424,10 @@ __device__ __forceinline__ void dec8_query_put(const Decode8Args& a, const uint4
 
 // The new tokens are seen by some rows only (causal, Nq > 1), and NaN among their values must
 // not reach the others as 0 x NaN. A warp of its own (within the softmax's loop the search cost
-// 3 %, here 1 %) looks through those rows of a V tile in shared memory before the products
-// read it: NaN codes become zeros, and `first` keeps, per byte of the tile's rows (lane: four
-// of them), the first such key, counted from `first_part` (the first key not seen by all;
-// 255: none). The rows that see that key get their NaN with the result.
+// 3 %, here 1 %; who tells whom of which tile: notice_ring.h) looks through those rows of a V tile
+// in shared memory before the products read it: NaN codes become zeros, and `first` keeps, per
+// byte of the tile's rows (lane: four of them), the first such key, counted from `first_part` (the
+// first key not seen by all; 255: none). The rows that see that key get their NaN with the result.
 __device__ __forceinline__ void dec8_hide_nan(uint8_t* tile, int key0, int first_part, int len, uint32_t& first) {
     const int lane = lane_id();
 #pragma unroll 1

@@ -29,10 +29,12 @@
 // each segment's queries. One CTA an SM: two fp16 V tiles, a ring of six code tiles, Q's
 // terms.
 //
-// Measured (16 x 8192 keys, 8 KV heads, d = 128, bf16): 119 us for 64 rows, 138 us for 128
-// (178 and 347 us in chunks of 16 rows); d = 64: 100 and 109 us. A tile takes 2,900 cycles, of
+// Measured (16 x 8192 keys, 8 KV heads, d = 128, bf16): 118 us for 64 rows, 136 us for 128
+// (178 and 347 us in chunks of 16 rows); d = 64: 103 and 114 us. A tile takes 2,900 cycles, of
 // which the pipe of the exponentials and conversions is busy for 2,050 (two softmax warps and
-// one of the expansion on an SM sub-partition). K expanded too: 146 and 168 us.
+// one of the expansion on an SM sub-partition). K expanded too: 146 and 168 us (when the codes'
+// S took 119 and 138). From 33 rows on (d = 64: 25) the 16-bit decode of the same shape is faster:
+// 105 and 122 us; d = 64: 89 and 103.
 #pragma once
 
 #include "fa_decode_fp8.cuh"

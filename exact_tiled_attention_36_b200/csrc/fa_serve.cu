@@ -108,8 +108,8 @@ fa_status append8(const void* k, const void* v, const long long* k_strides, cons
 }
 
 // More rows of a KV head than this take the form with the rows along M. Measured, 16 x 8192 keys
-// and 8 KV heads, in chunks (of 16 rows; d = 64: 8) against it: d = 128, 32 rows 98 us against 112,
-// 40 rows 137 against 112; d = 64, 24 rows 87 us against 95, 32 rows 111 against 96.
+// and 8 KV heads, in chunks (of 16 rows; d = 64: 8) against it: d = 128, 32 rows 96 us against 111,
+// 40 rows 138 against 108; d = 64, 24 rows 86 us against 98, 32 rows 109 against 98.
 int dec8_many_rows(int d) { return d == 64 ? 24 : 32; }
 
 // How a call's rows become items, and its workspace: meta (each item's first and last team), the

@@ -458,7 +458,8 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
  *       are not used. fa_cache_append_fp8 / fa_cache_append_paged_fp8 write both.
  *   workspace: device buffer of fa_decode_fp8_workspace_size(B,Hq,Hkv,Nq,d) bytes,
  *       16-byte aligned, owned by the caller (query it with the device the call will run
- *       on current; 0 when no device is visible).
+ *       on current; 0 when no device is visible). One call's at a time: calls or captured
+ *       graphs that may run at once need one each.
  * Every other argument, result and error is that of fa_decode / fa_decode_paged.
  */
 size_t fa_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
@@ -543,7 +544,8 @@ fa_status fa_cache_append_paged(const void* k, const void* v, const long long* k
  *   A sequence whose lengths do not fit (negative, more than max_new new tokens, past the
  *   capacity, tokens outside [0, total_new)) is left out, as is a block whose page lies
  *   outside [0, num_pages); the device error word then makes the next
- *   fa_get_last_device_error return FA_ERR_INVALID_ARG.
+ *   fa_get_last_device_error return FA_ERR_INVALID_ARG. With total_new, max_new or the
+ *   capacity 0 the call returns FA_OK and looks at no lengths.
  *   Tensors 16-byte aligned, factors and integers 4-byte; d is 64 or 128; page_size as
  *   fa_decode_paged.
  */
