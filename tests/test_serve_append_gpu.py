@@ -7,7 +7,7 @@ import torch
 from exact_tiled_attention_36_b200 import binding as fb
 from tests import serve_ref as ref
 from tests.gpu_util import f64
-from tests.test_serve_gpu import DT, I32, dev
+from tests.test_serve_gpu import DT, dev, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,17 @@ def test_append_among_blocks_without_a_page(page, d, dtype):
         want[kept], wf[kept] = codes[i][kept], fac[i][kept]
         assert np.array_equal(facs[i].cpu().numpy(), wf.astype(np.float32))
         assert np.array_equal(pools[i].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_append_of_a_prompt_beside_single_tokens(page):
+    """One long prompt, single tokens and idle sequences in one call."""
+    g = np.random.default_rng(page)
+    B = 40
+    counts = g.integers(0, 2, B).tolist()
+    counts[17] = 1900
+    olds = [int(g.integers(0, 140)) for _ in range(B)]
+    got_c, got_f, codes, fac = run_append((page, 2048, 2, 64, "bf16", olds, counts))
+    for i in range(2):
+        assert np.array_equal(got_f[i], fac[i])
+        assert np.array_equal(got_c[i], codes[i])

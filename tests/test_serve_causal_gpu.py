@@ -52,13 +52,14 @@ def one_tile(g, Nq, B):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("Hq,Nq", [(8, 4), (4, 7), (20, 4), (32, 7)])  # 16, 14, 40 and 112 rows of a KV head
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("Hq,Nq", [(8, 4), (4, 7), (20, 4), (32, 7), (2, 32), (2, 128)])  # 14 to 128 rows of a KV head
 @pytest.mark.parametrize("lengths,page,B", [(several_tiles, 0, 110), (several_tiles, 64, 110), (one_tile, 16, 600)])
-def test_causal_tiles_in_a_row(lengths, page, B, Hq, Nq, d):
+def test_causal_tiles_in_a_row(lengths, page, B, Hq, Nq, d, dtype):
     Hkv, g = 2, np.random.default_rng(Hq + Nq + d)
     lens = lengths(g, Nq, B)
     cache = BigCache(B, max(lens), Hkv, d, page, lens, seed=Hq + d)
-    q = queries(B, Nq, Hq, d, "bf16", 51)
+    q = queries(B, Nq, Hq, d, dtype, 51)
     bad = np.zeros((B, Nq, Hq, d), dtype=bool)
     put = []
     for b in range(0, B, 3):

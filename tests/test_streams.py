@@ -210,3 +210,46 @@ def test_other_helpers_on_another_stream(side):
         else:
             assert torch.equal(a, b), name
     del busy
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq", [8, 80])
+def test_captured_on_a_forked_stream(side, Hq):
+    """A call with `stream` inside a capture, on a stream that joined it: replayed over new contents, twice,
+    with eager calls on both streams between the replays."""
+    B, N, Hkv, d = 3, 700, 2, 128
+    data = [caches(B, N, Hkv, d, s) for s in (6, 7)]
+    q = torch.randn(B, 1, Hq, d, device="cuda").to(torch.bfloat16)
+    want = [fb.attention_decode_fp8(q, *x) for x in data]
+    lens, news = torch.tensor([5, 0], dtype=I32, device="cuda"), torch.tensor([20, 9], dtype=I32, device="cuda")
+    free, table = torch.arange(9, dtype=I32, device="cuda"), torch.zeros(2, 4, dtype=I32, device="cuda")
+    tables = [x.clone() for x in fb.build_block_tables(lens, news, free, table, 16, 9, 29)]
+    now = [x.clone() for x in data[0]]
+    here, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=here):
+        first = fb.attention_decode_fp8(q, *now)
+        side.wait_stream(here)
+        forked = fb.attention_decode_fp8(q, *now, stream=side)
+        built = fb.build_block_tables(lens, news, free, table, 16, 9, 29, stream=side)
+        beside = fb.attention_decode_fp8(q, *now)
+        here.wait_stream(side)
+        fb.attention_decode_fp8(q, *now, stream=side)  # its results dropped within the capture
+        here.wait_stream(side)
+        last = fb.attention_decode_fp8(q, *now)
+    for i in (1, 0, 1):
+        for x, y in zip(now, data[i]):
+            x.copy_(y)
+        side.wait_stream(torch.cuda.current_stream())
+        eager = fb.attention_decode_fp8(q, *data[1 - i]), fb.attention_decode_fp8(q, *data[1 - i], stream=side)
+        torch.cuda.synchronize()
+        for x in (first, forked, beside, last):
+            for t in x:
+                t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x in (first, forked, beside, last):
+            assert torch.equal(x[0], want[i][0]) and torch.equal(x[1], want[i][1])
+        for x in eager:
+            assert torch.equal(x[0], want[1 - i][0]) and torch.equal(x[1], want[1 - i][1])
+        assert all(torch.equal(a, b) for a, b in zip(built, tables))
